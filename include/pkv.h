@@ -391,6 +391,143 @@ pkv_status pkv_block_hashes(const int32_t* token_ids, const int64_t* cu_tokens, 
                             int32_t block_size, const int64_t* out_offsets, uint64_t* hashes,
                             int64_t hashes_capacity, int32_t* device_error, void* stream);
 
+/*
+ * Plan a step on the GPU: block tables, lengths and the slot map from the
+ * request lengths, by the rules of the host block manager ("3.3
+ * 批处理与内存管理", sections "PagedAttention：块表" and "代码"), so that a
+ * step needs no host round trip and can be captured in a CUDA graph.
+ * Sequence s holds past_lens[s] tokens and takes new_lens[s] more (0: it sits
+ * the step out; 1: a decode token; more: a prompt or a chunk of one):
+ *   new blocks   ceil((past + new) / S) - ceil(past / S), taken from the top of
+ *                the free stack, sequence after sequence (the i-th id taken is
+ *                free_blocks[*free_count - 1 - i]) and written into the table
+ *                behind the blocks it has; other table entries are not touched
+ *   seq_lens[s]  past + new (the context_lens / kv_lens of the attention calls)
+ *   cu_q         [num_seqs + 1] exclusive sums of new_lens (nullable)
+ *   q_starts     [num_seqs] past_lens (nullable)
+ *   slot_mapping int64 [max_tokens]: token i of sequence s, at position p = past
+ *                + i, gets table[s][p / S] * S + p % S at index cu_q[s] + i;
+ *                entries past the step's tokens are -1 (padding tokens)
+ *   *new_free_count  *free_count less the blocks taken
+ * cu_q, q_starts and seq_lens are what pkv_paged_prefill_varlen and
+ * pkv_paged_attention_mixed take, slot_mapping what pkv_reshape_and_cache takes.
+ * seq_lens may be past_lens and new_free_count may be free_count (in place); the
+ * other arrays must not overlap.  free_blocks has room for num_blocks ids.
+ *
+ * A sequence on a shared prefix starts with the prefix's block ids in its table
+ * row and past_lens = the prefix's length, a multiple of the block size (the
+ * call writes into a sequence's last block when it is partly filled, so such a
+ * block must be the sequence's own).
+ *
+ * All or nothing: a negative length, one beyond max_blocks_per_seq * S, or more
+ * tokens than max_tokens sets PKV_DEVERR_BAD_LENGTH, and a step that needs more
+ * blocks than are free (or a count outside [0, num_blocks]) sets
+ * PKV_DEVERR_BAD_SLOT; then no table entry changes, seq_lens and *new_free_count
+ * are the old values, cu_q is 0 and every slot -1.  An id outside the pool, taken
+ * from the free stack or found in the table's partly filled block, sets
+ * PKV_DEVERR_BAD_BLOCK, and its tokens get slot -1 (its new table entry -1).
+ * Supported: block_size 4/8/16/32, num_seqs <= 8192.
+ */
+pkv_status pkv_extend_sequences(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* past_lens,
+                                const int32_t* new_lens, int32_t num_seqs, int32_t block_size,
+                                const int32_t* free_blocks, const int32_t* free_count, int32_t num_blocks,
+                                int32_t* seq_lens, int32_t* new_free_count, int64_t* slot_mapping,
+                                int32_t max_tokens, int32_t* cu_q, int32_t* q_starts, int32_t* device_error,
+                                void* stream);
+
+/*
+ * The mirror image: every sequence with finished[s] != 0 hands its blocks back.
+ * Its table entries [keep_blocks[s], ceil(past_lens[s] / S)) go on top of the
+ * free stack, in order and sequence after sequence; seq_lens[s] = 0 for it and
+ * past_lens[s] for the others; *new_free_count = *free_count plus the blocks
+ * handed back.  keep_blocks (nullable: 0) are leading blocks that are not the
+ * sequence's own (a shared prefix that stays).  The table is not changed; its
+ * entries past a sequence's length are never read.
+ * seq_lens may be past_lens and new_free_count may be free_count.
+ * Errors, all or nothing: a length outside [0, max_blocks_per_seq * S] or a
+ * negative keep_blocks sets PKV_DEVERR_BAD_LENGTH, a stack that would grow past
+ * num_blocks PKV_DEVERR_BAD_SLOT; then the stack and its count stay and seq_lens is
+ * past_lens.  A table entry outside the pool sets PKV_DEVERR_BAD_BLOCK and is
+ * handed back as -1, which pkv_extend_sequences reports when it takes it.
+ */
+pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* past_lens,
+                                 const uint8_t* finished, const int32_t* keep_blocks, int32_t num_seqs,
+                                 int32_t block_size, int32_t* free_blocks, const int32_t* free_count,
+                                 int32_t num_blocks, int32_t* seq_lens, int32_t* new_free_count,
+                                 int32_t* device_error, void* stream);
+
+/*
+ * Paged decode attention (one query token per sequence) for a batch in which
+ * groups of sequences share a long prefix ("3.3 批处理与内存管理", section
+ * "共享与写时复制"): the prefix is read and multiplied once for the whole group,
+ * its query rows stacked, instead of once per sequence as by
+ * pkv_paged_attention_decode_shared.  Same result as pkv_paged_attention_decode
+ * up to rounding: softmax(scale * q . K^T) V over all of a sequence's positions,
+ * the prefix's and its own parts joined by
+ *   M = max(m_p, m_s), l = e^(m_p - M) l_p + e^(m_s - M) l_s, O likewise, out = O / l.
+ *   cu_groups:   [num_groups + 1] device int32: group g holds the sequences
+ *                [cu_groups[g], cu_groups[g + 1]); every sequence is in one group.
+ *   prefix_lens: [num_groups] device int32: tokens shared by the whole group, a
+ *                multiple of block_size (only full blocks are shared), 0 for none,
+ *                and no more than the context length of any of its sequences.
+ * The prefix is read through the table row of the group's first sequence; the
+ * other rows' first prefix_lens / block_size entries are not read.
+ * A sequence whose group or lengths break these rules sets PKV_DEVERR_BAD_LENGTH;
+ * its row is zero, or undefined where the group's own sizes are malformed.
+ *   workspace: >= pkv_paged_attention_decode_prefix_workspace_size bytes, 16-byte
+ *        aligned; concurrent calls must not share it.
+ * Arithmetic: the prefix as pkv_paged_prefill_chunk, the rest as
+ * pkv_paged_attention_decode_shared (per cache type), both in fp32 sums.
+ * Supported: bf16 queries, bf16, FP8 or INT8 cache, head_dim 128, block_size
+ *   8/16/32, G in {1, 2, 4, 8}, num_seqs <= 8192, num_groups <= 2048, scale
+ *   positive.  Two kernels, the second launched while the first runs.
+ */
+pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, int32_t q_dtype, const void* k_cache,
+                                             const void* v_cache, const pkv_cache_desc* cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                             float scale, const int32_t* cu_groups, const int32_t* prefix_lens,
+                                             int32_t num_groups, void* workspace, size_t workspace_bytes,
+                                             int32_t* device_error, void* stream);
+
+/* Bytes of device workspace pkv_paged_attention_decode_prefix needs (on the current device). */
+pkv_status pkv_paged_attention_decode_prefix_workspace_size(const pkv_cache_desc* cache, int32_t num_seqs,
+                                                            int32_t num_q_heads, size_t* bytes);
+
+/*
+ * Cross attention: decoder queries against the states of an encoder, of another
+ * length, kept in the paged cache (written once by pkv_reshape_and_cache).  No
+ * mask but the length: query token i of sequence s and query head hq (KV head
+ * hq / G) give
+ *   out = softmax(scale * q . K_s^T) V_s   over the positions [0, kv_lens[s])
+ * gathered through block table row s.  A sequence without states (kv_lens[s] = 0)
+ * gets zero rows.
+ *   cu_q: [num_seqs + 1] device int32, non-decreasing: sequence s owns query
+ *        tokens [cu_q[s], cu_q[s + 1]) (a decoder prompt; the beams or samples
+ *        that share one encoder input), at most total_q_tokens.  Rows that no
+ *        sequence owns are not written.
+ *        NULL: one query token a sequence (total_q_tokens = num_seqs), the decode
+ *        step; this form has the types, shapes and limits of
+ *        pkv_paged_attention_decode, which computes it.
+ *   workspace: >= pkv_paged_cross_attention_workspace_size bytes, 16-byte
+ *        aligned; concurrent calls must not share it.
+ * Arithmetic with cu_q: that of pkv_paged_prefill_chunk per cache type.
+ * A malformed cu_q range or a length outside [0, max_blocks_per_seq * S] sets
+ * PKV_DEVERR_BAD_LENGTH and leaves that sequence's rows unwritten; a table entry
+ * outside the pool sets PKV_DEVERR_BAD_BLOCK.
+ * Supported with cu_q: bf16 queries, bf16, FP8 or INT8 cache, head_dim 128,
+ *   block_size 8/16/32, G dividing 128, num_seqs <= 2048, scale positive.
+ */
+pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
+                                     const int32_t* cu_q, const int32_t* kv_lens, const void* k_cache,
+                                     const void* v_cache, const pkv_cache_desc* cache, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                     void* workspace, size_t workspace_bytes, int32_t* device_error, void* stream);
+
+/* Bytes of device workspace pkv_paged_cross_attention needs (on the current device), in either form. */
+pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
+                                                    int32_t num_seqs, int32_t num_q_heads, size_t* bytes);
+
 /* Human-readable name of a status code (static storage). */
 const char* pkv_status_string(pkv_status status);
 

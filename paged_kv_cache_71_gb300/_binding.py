@@ -79,9 +79,19 @@ def lib() -> ctypes.CDLL:
     L.pkv_paged_attention_mixed_workspace_size.argtypes = [D, i32, i32, ctypes.POINTER(sz)]
     L.pkv_swap_blocks.argtypes = [P, P, i32, P, P, i32, D, P, i32, P, P]
     L.pkv_block_hashes.argtypes = [P, P, i32, i32, P, P, ctypes.c_int64, P, P]
+    L.pkv_extend_sequences.argtypes = [P, i32, P, P, i32, i32, P, P, i32, P, P, P, i32, P, P, P, P]
+    L.pkv_release_sequences.argtypes = [P, i32, P, P, P, i32, i32, P, P, i32, P, P, P, P]
+    L.pkv_paged_attention_decode_prefix.argtypes = [P, P, i32, P, P, D, P, i32, P, i32, i32, f32, P, P, i32, P, sz,
+                                                    P, P]
+    L.pkv_paged_attention_decode_prefix_workspace_size.argtypes = [D, i32, i32, ctypes.POINTER(sz)]
+    L.pkv_paged_cross_attention.argtypes = [P, P, i32, i32, P, P, P, P, D, P, i32, i32, i32, f32, P, sz, P, P]
+    L.pkv_paged_cross_attention_workspace_size.argtypes = [D, i32, i32, i32, ctypes.POINTER(sz)]
     for name in ("pkv_reshape_and_cache", "pkv_paged_attention_workspace_size", "pkv_paged_attention_decode",
                  "pkv_copy_blocks", "pkv_paged_attention_decode_static_scratch", "pkv_paged_prefill_chunk",
-                 "pkv_paged_prefill_varlen", "pkv_swap_blocks", "pkv_block_hashes"):
+                 "pkv_paged_prefill_varlen", "pkv_swap_blocks", "pkv_block_hashes", "pkv_extend_sequences",
+                 "pkv_release_sequences", "pkv_paged_attention_decode_prefix",
+                 "pkv_paged_attention_decode_prefix_workspace_size", "pkv_paged_cross_attention",
+                 "pkv_paged_cross_attention_workspace_size"):
         getattr(L, name).restype = ctypes.c_int
     L.pkv_status_string.argtypes = [ctypes.c_int]
     L.pkv_status_string.restype = ctypes.c_char_p
@@ -246,6 +256,125 @@ def pkv_block_hashes(token_ids, cu_tokens, block_size: int, out_offsets, hashes,
                                   _ptr(out_offsets), _ptr(hashes), int(hashes.numel()), _ptr(device_error),
                                   _stream(stream)),
            "pkv_block_hashes")
+
+
+def _expect(func: str, **tensors) -> None:
+    """Refuse tensors that the pointers alone would not tell from good ones: name=(tensor, dtypes, shape), a None in the
+    shape standing for any size.  Layouts must be contiguous, and every tensor on the current CUDA device."""
+    for name, (t, dtypes, shape) in tensors.items():
+        if t.dtype not in dtypes:
+            raise PkvError(1, func, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected "
+                                    f"{tuple('any' if n is None else n for n in shape)}")
+        if not t.is_contiguous():
+            raise PkvError(1, func, f"{name} must be contiguous")
+    for name, (t, _, _) in tensors.items():
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
+
+
+_I32, _I64, _FLAG = (torch.int32,), (torch.int64,), (torch.bool, torch.uint8)
+_FLOATS, _CACHES = (torch.float32, torch.bfloat16), tuple(_DTYPE_CODE)
+
+
+def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, free_blocks, free_count, seq_lens,
+                         new_free_count, slot_mapping, cu_q=None, q_starts=None, device_error=None,
+                         stream=None) -> None:
+    """Block tables, lengths and slot map of a step from the request lengths, on the GPU.  seq_lens may be past_lens and
+    new_free_count may be free_count (in place); free_blocks has one entry per block of the pool."""
+    L, n = lib(), past_lens.shape[0]
+    want = dict(block_tables=(block_tables, _I32, (n, None)), past_lens=(past_lens, _I32, (n,)),
+                new_lens=(new_lens, _I32, (n,)), free_blocks=(free_blocks, _I32, (None,)),
+                free_count=(free_count, _I32, (1,)), seq_lens=(seq_lens, _I32, (n,)),
+                new_free_count=(new_free_count, _I32, (1,)), slot_mapping=(slot_mapping, _I64, (None,)))
+    if cu_q is not None:
+        want["cu_q"] = (cu_q, _I32, (n + 1,))
+    if q_starts is not None:
+        want["q_starts"] = (q_starts, _I32, (n,))
+    _expect("pkv_extend_sequences", **want)
+    _check(L.pkv_extend_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(new_lens), n,
+                                  int(block_size), _ptr(free_blocks), _ptr(free_count), free_blocks.shape[0],
+                                  _ptr(seq_lens), _ptr(new_free_count), _ptr(slot_mapping), slot_mapping.shape[0],
+                                  _ptr(cu_q), _ptr(q_starts), _ptr(device_error), _stream(stream)),
+           "pkv_extend_sequences")
+
+
+def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, free_blocks, free_count, seq_lens,
+                          new_free_count, keep_blocks=None, device_error=None, stream=None) -> None:
+    """Finished sequences hand their blocks back to the free stack, on the GPU (finished: bool or uint8 [num_seqs])."""
+    L, n = lib(), past_lens.shape[0]
+    want = dict(block_tables=(block_tables, _I32, (n, None)), past_lens=(past_lens, _I32, (n,)),
+                finished=(finished, _FLAG, (n,)), free_blocks=(free_blocks, _I32, (None,)),
+                free_count=(free_count, _I32, (1,)), seq_lens=(seq_lens, _I32, (n,)),
+                new_free_count=(new_free_count, _I32, (1,)))
+    if keep_blocks is not None:
+        want["keep_blocks"] = (keep_blocks, _I32, (n,))
+    _expect("pkv_release_sequences", **want)
+    _check(L.pkv_release_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(finished),
+                                   _ptr(keep_blocks), n, int(block_size), _ptr(free_blocks), _ptr(free_count),
+                                   free_blocks.shape[0], _ptr(seq_lens), _ptr(new_free_count), _ptr(device_error),
+                                   _stream(stream)),
+           "pkv_release_sequences")
+
+
+def pkv_paged_attention_decode_prefix_workspace_size(cache: CacheDesc, num_seqs: int, num_q_heads: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pkv_paged_attention_decode_prefix_workspace_size(ctypes.byref(cache), int(num_seqs),
+                                                                  int(num_q_heads), ctypes.byref(out)),
+           "pkv_paged_attention_decode_prefix_workspace_size")
+    return int(out.value)
+
+
+def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc, block_tables, context_lens,
+                                      cu_groups, prefix_lens, scale: float, workspace=None, device_error=None,
+                                      stream=None) -> None:
+    """Decode attention for groups of sequences (cu_groups) that share their first prefix_lens tokens' blocks: a group's
+    prefix is computed once for all of its sequences."""
+    L, (n, heads, D) = lib(), q.shape
+    caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
+    groups = prefix_lens.shape[0]
+    _expect("pkv_paged_attention_decode_prefix", q=(q, _FLOATS, (n, heads, cache.head_dim)),
+            out=(out, (q.dtype,), (n, heads, D)), k_cache=(k_cache, _CACHES, caches),
+            v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, None)),
+            context_lens=(context_lens, _I32, (n,)), cu_groups=(cu_groups, _I32, (groups + 1,)),
+            prefix_lens=(prefix_lens, _I32, (groups,)))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(L.pkv_paged_attention_decode_prefix(_ptr(out), _ptr(q), _dtype(q), _ptr(k_cache), _ptr(v_cache),
+                                               ctypes.byref(cache), _ptr(block_tables), block_tables.shape[1],
+                                               _ptr(context_lens), n, heads, float(scale), _ptr(cu_groups),
+                                               _ptr(prefix_lens), groups, _ptr(workspace), ws_bytes,
+                                               _ptr(device_error), _stream(stream)),
+           "pkv_paged_attention_decode_prefix")
+
+
+def pkv_paged_cross_attention_workspace_size(cache: CacheDesc, total_q_tokens: int, num_seqs: int,
+                                             num_q_heads: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pkv_paged_cross_attention_workspace_size(ctypes.byref(cache), int(total_q_tokens), int(num_seqs),
+                                                          int(num_q_heads), ctypes.byref(out)),
+           "pkv_paged_cross_attention_workspace_size")
+    return int(out.value)
+
+
+def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: CacheDesc, block_tables, scale: float,
+                              workspace=None, device_error=None, stream=None) -> None:
+    """Decoder queries against paged encoder states, without a mask: sequence s owns query tokens
+    [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
+    L, (tokens, heads, D), n = lib(), q.shape, kv_lens.shape[0]
+    caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
+    want = dict(q=(q, _FLOATS, (tokens, heads, cache.head_dim)), out=(out, (q.dtype,), (tokens, heads, D)),
+                kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _CACHES, caches),
+                v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, None)))
+    if cu_q is not None:
+        want["cu_q"] = (cu_q, _I32, (n + 1,))
+    _expect("pkv_paged_cross_attention", **want)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(L.pkv_paged_cross_attention(_ptr(out), _ptr(q), _dtype(q), tokens, _ptr(cu_q), _ptr(kv_lens),
+                                       _ptr(k_cache), _ptr(v_cache), ctypes.byref(cache), _ptr(block_tables),
+                                       block_tables.shape[1], n, heads, float(scale), _ptr(workspace), ws_bytes,
+                                       _ptr(device_error), _stream(stream)),
+           "pkv_paged_cross_attention")
 
 
 def pkv_status_string(status: int) -> str:

@@ -11,8 +11,10 @@
 #include "cache_ops.cuh"
 #include "decode.cuh"
 #include "decode_mma.cuh"
+#include "full_tile.cuh"
 #include "mixed.cuh"
 #include "prefill.cuh"
+#include "tables.cuh"
 
 namespace pkv {
 
@@ -61,6 +63,24 @@ PKV_EXTERN_MIX_G(1, KvE4M3)
 PKV_EXTERN_MIX_G(2, KvI8)
 #undef PKV_EXTERN_MIX_G
 #undef PKV_EXTERN_MIX
+
+// The shared-prefix decode's instantiations live in decode_prefix_{bf16,fp8,i8}_s{8,16,32}.cu.
+#define PKV_EXTERN_PFX(S_, KV_, G_, HP_)                                                                    \
+    extern template cudaError_t launch_paged_decode_prefix<G_, S_, KV_, HP_>(                               \
+        const CUtensorMap&, const CUtensorMap&, const DecodeArgs&, const PrefixArgs&, int, int, size_t, cudaStream_t);
+#define PKV_EXTERN_PFX_1(S_, KV_)                                                                           \
+    PKV_EXTERN_PFX(S_, KV_, 1, 1) PKV_EXTERN_PFX(S_, KV_, 2, 1) PKV_EXTERN_PFX(S_, KV_, 4, 1) PKV_EXTERN_PFX(S_, KV_, 8, 1)
+#define PKV_EXTERN_PFX_2(S_, KV_) PKV_EXTERN_PFX(S_, KV_, 1, 2) PKV_EXTERN_PFX(S_, KV_, 2, 2) PKV_EXTERN_PFX(S_, KV_, 4, 2)
+#define PKV_EXTERN_PFX_S(S_)                                                                                \
+    PKV_EXTERN_PFX_1(S_, KvBF16) PKV_EXTERN_PFX_1(S_, KvE4M3) PKV_EXTERN_PFX_1(S_, KvI8)                     \
+    PKV_EXTERN_PFX_2(S_, KvE4M3) PKV_EXTERN_PFX_2(S_, KvI8)
+PKV_EXTERN_PFX_S(8)
+PKV_EXTERN_PFX_S(16)
+PKV_EXTERN_PFX_S(32)
+#undef PKV_EXTERN_PFX_S
+#undef PKV_EXTERN_PFX_2
+#undef PKV_EXTERN_PFX_1
+#undef PKV_EXTERN_PFX
 
 // ------------------------------------------------------------------ error detail
 
@@ -1007,5 +1027,438 @@ PKV_API pkv_status pkv_paged_attention_mixed(void* out, const void* q, int32_t q
         : nk == 1 ? dispatch_mixed<1, KvE4M3>(G, qm, km, vm, pa, da, ma, di.sms, smem, s)
                   : dispatch_mixed<2, KvI8>(G, qm, km, vm, pa, da, ma, di.sms, smem, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attention_mixed launch");
+    return PKV_OK;
+}
+
+// ------------------------------------------------------------------ step planning
+
+// Checks that both step-planning calls share.
+static pkv_status check_tables(int32_t max_blocks_per_seq, int32_t num_seqs, int32_t block_size, int32_t num_blocks) {
+    if (max_blocks_per_seq <= 0 || num_seqs < 0 || num_blocks <= 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (num_seqs=%d max_blocks_per_seq=%d num_blocks=%d)", num_seqs,
+                    max_blocks_per_seq, num_blocks);
+    if (block_size != 4 && block_size != 8 && block_size != 16 && block_size != 32)
+        return fail(PKV_ERR_UNSUPPORTED, "block_size %d (supported: 4, 8, 16, 32)", block_size);
+    if (num_seqs > kMaxTableSeqs) return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > %d", num_seqs, kMaxTableSeqs);
+    if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
+        return fail(PKV_ERR_OUT_OF_RANGE, "num_blocks * block_size exceeds 2^31-1");
+    if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq > INT32_MAX ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX - 64)
+        return fail(PKV_ERR_OUT_OF_RANGE, "block table larger than 2^31-1 entries or 2^31-65 tokens a row");
+    return PKV_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static int log2_of(int s) { return s == 4 ? 2 : s == 8 ? 3 : s == 16 ? 4 : 5; }
+
+PKV_API pkv_status pkv_extend_sequences(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* past_lens,
+                                        const int32_t* new_lens, int32_t num_seqs, int32_t block_size,
+                                        const int32_t* free_blocks, const int32_t* free_count, int32_t num_blocks,
+                                        int32_t* seq_lens, int32_t* new_free_count, int64_t* slot_mapping,
+                                        int32_t max_tokens, int32_t* cu_q, int32_t* q_starts, int32_t* device_error,
+                                        void* stream) {
+    g_detail[0] = 0;
+    pkv_status st = check_tables(max_blocks_per_seq, num_seqs, block_size, num_blocks);
+    if (st != PKV_OK) return st;
+    if (max_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "max_tokens %d < 0", max_tokens);
+    if (max_tokens > INT32_MAX - 64) return fail(PKV_ERR_OUT_OF_RANGE, "max_tokens %d > 2^31-65", max_tokens);
+    if ((num_seqs > 0 && (!block_tables || !past_lens || !new_lens || !seq_lens)) || !free_blocks || !free_count ||
+        !new_free_count || (max_tokens > 0 && !slot_mapping))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(block_tables) || !aligned4(past_lens) || !aligned4(new_lens) || !aligned4(free_blocks) ||
+        !aligned4(free_count) || !aligned4(seq_lens) || !aligned4(new_free_count) || !aligned4(cu_q) ||
+        !aligned4(q_starts) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned, slot_mapping 8-byte");
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    ExtendArgs a{block_tables, past_lens, new_lens, free_blocks, free_count, seq_lens, new_free_count, cu_q, q_starts,
+                 slot_mapping, device_error, num_seqs, max_blocks_per_seq, log2_of(block_size), num_blocks, max_tokens};
+    const cudaError_t e = launch_extend_sequences(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "extend_sequences launch");
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* past_lens, const uint8_t* finished, const int32_t* keep_blocks,
+                                         int32_t num_seqs, int32_t block_size, int32_t* free_blocks,
+                                         const int32_t* free_count, int32_t num_blocks, int32_t* seq_lens,
+                                         int32_t* new_free_count, int32_t* device_error, void* stream) {
+    g_detail[0] = 0;
+    pkv_status st = check_tables(max_blocks_per_seq, num_seqs, block_size, num_blocks);
+    if (st != PKV_OK) return st;
+    if ((num_seqs > 0 && (!block_tables || !past_lens || !finished || !seq_lens)) || !free_blocks || !free_count ||
+        !new_free_count)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(block_tables) || !aligned4(past_lens) || !aligned4(keep_blocks) || !aligned4(free_blocks) ||
+        !aligned4(free_count) || !aligned4(seq_lens) || !aligned4(new_free_count))
+        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    ReleaseArgs a{block_tables, past_lens, finished, keep_blocks, free_blocks, free_count, seq_lens, new_free_count,
+                  device_error, num_seqs, max_blocks_per_seq, log2_of(block_size), num_blocks};
+    const cudaError_t e = launch_release_sequences(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "release_sequences launch");
+    return PKV_OK;
+}
+
+// ------------------------------------------------------------------ attention without a mask: shared prefixes, cross
+
+// Scratch of the unmasked tile (full_tile.cu): the cut items and the share, the sequences' plan (shared prefixes), then
+// the partial records' (m, l) and O, one row per (query token, query head) and 256 per CTA.
+struct FullScratch {
+    size_t cuts, share, plan, ml, o, total;  // byte offsets, and the whole
+};
+static FullScratch full_scratch(int sms, int tokens, int Hq, int plan_seqs) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = static_cast<size_t>(tokens) * Hq + static_cast<size_t>(sms) * 256;
+    FullScratch f;
+    f.cuts = 0;
+    f.share = up(static_cast<size_t>(sms) * 16);
+    f.plan = f.share + 256;
+    f.ml = f.plan + up(static_cast<size_t>(plan_seqs) * 16);
+    f.o = f.ml + up(rows * 8);
+    f.total = f.o + rows * 512;
+    return f;
+}
+
+static FullArgs full_args(const FullScratch& f, void* base, int tokens, int Hq, bool prefix) {
+    uint8_t* p = static_cast<uint8_t*>(base);
+    FullArgs a;
+    a.rec_o = reinterpret_cast<float*>(p + f.o);
+    a.rec_ml = reinterpret_cast<float2*>(p + f.ml);
+    a.extra_row = static_cast<int64_t>(tokens) * Hq;
+    a.cuts = reinterpret_cast<int4*>(p + f.cuts);
+    a.seq_plan = prefix ? reinterpret_cast<int4*>(p + f.plan) : nullptr;
+    a.share = reinterpret_cast<int*>(p + f.share);
+    a.prefix = prefix;
+    return a;
+}
+
+// The unmasked tile's checks of types and shapes.
+static pkv_status check_full(const char* what, int32_t q_dtype, const pkv_cache_desc& c, int32_t num_q_heads, int max_g,
+                             int* G_out) {
+    if (num_q_heads % c.num_kv_heads != 0)
+        return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", num_q_heads, c.num_kv_heads);
+    const int G = num_q_heads / c.num_kv_heads;
+    if (q_dtype != PKV_BF16 || (c.dtype != PKV_BF16 && !narrow(c.dtype)))
+        return fail(PKV_ERR_UNSUPPORTED, "%s supports bf16 queries with a bf16, FP8 or INT8 cache", what);
+    if (c.head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "%s supports head_dim 128", what);
+    if (c.block_size < 8) return fail(PKV_ERR_UNSUPPORTED, "%s supports block_size 8, 16, 32", what);
+    if (G > max_g || 128 % G != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "GQA group %d must divide 128 and be at most %d", G, max_g);
+    if (c.num_kv_heads > 1024) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 1024", c.num_kv_heads);
+    *G_out = G;
+    return PKV_OK;
+}
+
+// The tile's arguments and tensor maps for `chunks` runs of query tokens.
+static pkv_status full_setup(PrefillArgs* out_a, CUtensorMap* qm, CUtensorMap* km, CUtensorMap* vm, void* out, const void* q,
+                             const void* k_cache, const void* v_cache, const pkv_cache_desc& c, int tokens, int Hq,
+                             const int32_t* cu, const int32_t* kv_lens, int chunks, const int32_t* tables, int MB,
+                             float scale, int32_t* err) {
+    const int Hkv = c.num_kv_heads, S = c.block_size, G = Hq / Hkv;
+    const bool nar = narrow(c.dtype);
+    const float kLog2e = 1.4426950408889634f;
+    // key tiles of the whole stream, at most: the kernel counts them in 32 bits
+    const int64_t kt = (static_cast<int64_t>(MB) * S + 63) / 64;
+    if ((static_cast<int64_t>(tokens) / (2 * (128 / G)) + chunks) * Hkv * kt > INT32_MAX - 4096)
+        return fail(PKV_ERR_OUT_OF_RANGE, "query tiles * num_kv_heads * key tiles must stay below 2^31");
+    PrefillArgs a;
+    a.out = out;
+    a.block_table = tables;
+    a.err = err;
+    a.NQ = tokens;
+    a.q_start = 0;
+    a.kv_len = 0;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = G;
+    a.S = S;
+    a.NB = c.num_blocks;
+    a.n_table = MB;
+    a.sm_log2 = scale * kLog2e * (nar ? c.k_scale : 1.f);
+    a.out_mul = nar ? c.v_scale : 1.f;
+    a.sm_base = scale * kLog2e;
+    a.k_head = c.k_head_scales;
+    a.v_head = c.v_head_scales;
+    a.timeout_ns = 2000000000ull;
+    a.nseq = chunks;
+    a.MB = MB;
+    a.cu_q = cu;
+    a.kv_lens = kv_lens;
+    *out_a = a;
+    pkv_status st;
+    if ((st = tensor_map_sw128(qm, q, false, 128, Hq, tokens, G, 128 / G)) != PKV_OK) return st;
+    const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * S;
+    if ((st = tensor_map_sw128(km, k_cache, nar, 128, Hkv, rows, 1, S)) != PKV_OK) return st;
+    return tensor_map_sw128(vm, v_cache, nar, 128, Hkv, rows, 1, S);
+}
+
+static int narrow_kind(int dtype) { return dtype == PKV_INT8 ? 2 : narrow(dtype) ? 1 : 0; }
+
+// KV heads per work unit of the shared-prefix decode's own blocks: as in the regular decode for one-byte caches, one for
+// bf16 (a pair's 16 KB stages leave room for 4 warps per SM only).
+static int prefix_heads_per_unit(int G, int Hkv, int dtype) {
+    return dtype == PKV_BF16 ? 1 : mma_heads_per_unit(G, Hkv, dtype);
+}
+
+// Scratch of the shared-prefix decode: the unmasked tile's, then the decode's counters and records.
+static size_t prefix_decode_offset(int sms, int B, int Hq) {
+    return (full_scratch(sms, B, Hq, B).total + 255) / 256 * 256;
+}
+static size_t prefix_workspace_bytes(int sms, int B, int Hq, int Hkv, int dtype) {
+    const int G = Hq / Hkv;
+    const size_t tickets = ((static_cast<size_t>(B) * Hkv * 4 + 255) / 256) * 256;
+    const size_t rows = static_cast<size_t>(G) * prefix_heads_per_unit(G, Hkv, dtype);
+    return prefix_decode_offset(sms, B, Hq) + tickets + static_cast<size_t>(sms) * kMmaWarps * 2 * rows * (128 + 2) * 4;
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_prefix_workspace_size(const pkv_cache_desc* cache, int32_t num_seqs,
+                                                                    int32_t num_q_heads, size_t* bytes) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (!bytes) return fail(PKV_ERR_INVALID_ARG, "bytes is NULL");
+    if (num_seqs < 0 || num_q_heads <= 0) 
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (num_seqs=%d num_q_heads=%d)", num_seqs, num_q_heads);
+    int G;
+    if ((st = check_full("the shared-prefix decode", PKV_BF16, *cache, num_q_heads, 8, &G)) != PKV_OK) return st;
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    *bytes = prefix_workspace_bytes(di.sms, num_seqs, num_q_heads, cache->num_kv_heads, cache->dtype);
+    return PKV_OK;
+}
+
+template <class KV>
+static cudaError_t dispatch_prefix(int S, int G, int HP, const CUtensorMap& km, const CUtensorMap& vm, const DecodeArgs& a,
+                                   const PrefixArgs& px, int grid, int block, size_t smem, cudaStream_t s) {
+#define PKV_PFX_G1(S_)                                                                                        \
+    switch (G) {                                                                                              \
+        case 1: return launch_paged_decode_prefix<1, S_, KV, 1>(km, vm, a, px, grid, block, smem, s);         \
+        case 2: return launch_paged_decode_prefix<2, S_, KV, 1>(km, vm, a, px, grid, block, smem, s);         \
+        case 4: return launch_paged_decode_prefix<4, S_, KV, 1>(km, vm, a, px, grid, block, smem, s);         \
+        case 8: return launch_paged_decode_prefix<8, S_, KV, 1>(km, vm, a, px, grid, block, smem, s);         \
+        default: return cudaErrorInvalidValue;                                                                \
+    }
+#define PKV_PFX_G2(S_)                                                                                        \
+    switch (G) {                                                                                              \
+        case 1: return launch_paged_decode_prefix<1, S_, KV, 2>(km, vm, a, px, grid, block, smem, s);         \
+        case 2: return launch_paged_decode_prefix<2, S_, KV, 2>(km, vm, a, px, grid, block, smem, s);         \
+        case 4: return launch_paged_decode_prefix<4, S_, KV, 2>(km, vm, a, px, grid, block, smem, s);         \
+        default: return cudaErrorInvalidValue;                                                                \
+    }
+    if constexpr (KV::es == 1) {
+        if (HP == 2) {
+            if (S == 8) PKV_PFX_G2(8)
+            if (S == 16) PKV_PFX_G2(16)
+            PKV_PFX_G2(32)
+        }
+    }
+    if (S == 8) PKV_PFX_G1(8)
+    if (S == 16) PKV_PFX_G1(16)
+    PKV_PFX_G1(32)
+#undef PKV_PFX_G1
+#undef PKV_PFX_G2
+}
+
+PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, int32_t q_dtype, const void* k_cache,
+                                                     const void* v_cache, const pkv_cache_desc* cache,
+                                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                     const int32_t* context_lens, int32_t num_seqs,
+                                                     int32_t num_q_heads, float scale, const int32_t* cu_groups,
+                                                     const int32_t* prefix_lens, int32_t num_groups, void* workspace,
+                                                     size_t workspace_bytes, int32_t* device_error, void* stream) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    const int Hkv = cache->num_kv_heads, S = cache->block_size;
+    if (num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || num_groups < 0 || (num_groups == 0 && num_seqs > 0))
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (num_seqs=%d num_q_heads=%d max_blocks_per_seq=%d num_groups=%d)",
+                    num_seqs, num_q_heads, max_blocks_per_seq, num_groups);
+    int G;
+    if ((st = check_full("the shared-prefix decode", q_dtype, *cache, num_q_heads, 8, &G)) != PKV_OK) return st;
+    if (num_seqs > 8192) return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 8192", num_seqs);
+    if (num_groups > prefill_ws_max_seqs())
+        return fail(PKV_ERR_UNSUPPORTED, "num_groups %d > %d groups per call", num_groups, prefill_ws_max_seqs());
+    if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq * Hkv > INT32_MAX - 64)
+        return fail(PKV_ERR_OUT_OF_RANGE, "num_seqs * max_blocks_per_seq * num_kv_heads must stay below 2^31");
+    if (!(scale > 0.f && scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and positive");
+    if (num_seqs == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_groups || !prefix_lens)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PKV_ERR_INVALID_ARG, "q, out and the caches must be 16-byte aligned");
+    if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(cu_groups) || !aligned4(prefix_lens))
+        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    const size_t need = prefix_workspace_bytes(di.sms, num_seqs, num_q_heads, Hkv, cache->dtype);
+    if (!workspace || workspace_bytes < need)
+        return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    const bool b16 = cache->dtype == PKV_BF16, nar = narrow(cache->dtype);
+    const int nk = narrow_kind(cache->dtype);
+    if (static_cast<size_t>(di.smem_optin) < prefill_ws_smem_bytes(nk))
+        return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the prefix tile");
+
+    // ---- the prefixes, each for its whole group
+    PrefillArgs pa;
+    CUtensorMap qm, km, vm;
+    if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, num_seqs, num_q_heads, cu_groups,
+                         prefix_lens, num_groups, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
+        return st;
+    const FullArgs fa = full_args(full_scratch(di.sms, num_seqs, num_q_heads, num_seqs), workspace, num_seqs,
+                                  num_q_heads, true);
+
+    // ---- the sequences' own blocks
+    const float kLog2e = 1.4426950408889634f;
+    const int HP = prefix_heads_per_unit(G, Hkv, cache->dtype);
+    uint8_t* dws = static_cast<uint8_t*>(workspace) + prefix_decode_offset(di.sms, num_seqs, num_q_heads);
+    DecodeArgs da;
+    da.out = out;
+    da.q = q;
+    da.block_tables = block_tables;
+    da.context_lens = context_lens;
+    da.tickets = reinterpret_cast<int32_t*>(dws);
+    da.partials = reinterpret_cast<float*>(dws + ((static_cast<size_t>(num_seqs) * Hkv * 4 + 255) / 256) * 256);
+    da.err = device_error;
+    da.B = num_seqs;
+    da.Hq = num_q_heads;
+    da.Hkv = Hkv;
+    da.S = S;
+    da.MB = max_blocks_per_seq;
+    da.NB = cache->num_blocks;
+    da.part_blocks = 1;
+    da.q_mul = scale * kLog2e * (nar ? cache->k_scale : 1.f);
+    da.o_mul = nar ? cache->v_scale : 1.f;
+    da.q_base = scale * kLog2e;
+    da.k_head = cache->k_head_scales;
+    da.v_head = cache->v_head_scales;
+    da.timeout_ns = 2000000000ull;
+    const uint32_t tile = static_cast<uint32_t>((b16 ? 2 : 1) * std::max(S * 128, 1024));
+    da.kv_bytes = static_cast<uint32_t>(S * 128 * (b16 ? 2 : 1));
+    da.q_bytes = 0;
+    da.stage_bytes = 2 * HP * tile;
+    da.prefix_bytes = static_cast<uint32_t>(((2 * static_cast<size_t>(num_seqs) + 2) * 4 + 1023) / 1024 * 1024);
+    const size_t budget = static_cast<size_t>(di.smem_optin) - 256 - 1024;  // static shared memory, alignment slack
+    int nw = kMmaWarps, depth = 0;
+    while (nw >= 1) {
+        const size_t per_warp = budget > da.prefix_bytes ? (budget - da.prefix_bytes) / nw : 0;
+        depth = 6;  // the deepest pipeline whose region, rounded to 1024 bytes, fits
+        while (depth >= 2 && (static_cast<size_t>(depth) * da.stage_bytes + 8 * depth + 1023) / 1024 * 1024 > per_warp)
+            --depth;
+        if (depth >= 2) break;
+        nw >>= 1;
+    }
+    if (depth < 2) return fail(PKV_ERR_UNSUPPORTED, "shared memory too small for this block size and batch");
+    da.depth = depth;
+    da.warp_bytes = static_cast<uint32_t>((static_cast<size_t>(depth) * da.stage_bytes + 8 * depth + 1023) / 1024 * 1024);
+    const size_t smem = da.prefix_bytes + static_cast<size_t>(nw) * da.warp_bytes + 1024;
+    CUtensorMap kd, vd;
+    const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * S;
+    const uint64_t fetch = static_cast<uint64_t>(b16 ? 256 : 128 * HP);
+    if ((st = tensor_map_sw128(&kd, k_cache, nar, 128, Hkv, rows, 1, S, fetch)) != PKV_OK) return st;
+    if ((st = tensor_map_sw128(&vd, v_cache, nar, 128, Hkv, rows, 1, S, fetch)) != PKV_OK) return st;
+    PrefixArgs px;
+    px.cu_groups = cu_groups;
+    px.prefix_lens = prefix_lens;
+    px.num_groups = num_groups;
+    px.rec_o = fa.rec_o;
+    px.rec_ml = fa.rec_ml;
+    px.extra_row = fa.extra_row;
+    px.seq_plan = fa.seq_plan;
+    px.share = fa.share;
+
+    // the counters are cleared first: the decode follows the prefix kernel directly, so that it may start beside it
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(da.tickets, 0, static_cast<size_t>(num_seqs) * Hkv * 4, s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing split-KV counters");
+    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix launch");
+    e = nk == 0   ? dispatch_prefix<KvBF16>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s)
+        : nk == 1 ? dispatch_prefix<KvE4M3>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s)
+                  : dispatch_prefix<KvI8>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode launch");
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
+                                                            int32_t num_seqs, int32_t num_q_heads, size_t* bytes) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (!bytes) return fail(PKV_ERR_INVALID_ARG, "bytes is NULL");
+    const int Hkv = cache->num_kv_heads;
+    if (total_q_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_q_heads % Hkv != 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (total_q_tokens=%d num_seqs=%d num_q_heads=%d num_kv_heads=%d)",
+                    total_q_tokens, num_seqs, num_q_heads, Hkv);
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    const int G = num_q_heads / Hkv;
+    size_t need = full_scratch(di.sms, total_q_tokens, num_q_heads, 0).total;
+    if (total_q_tokens == num_seqs && (G == 1 || G == 2 || G == 4 || G == 8))  // may come as single tokens
+        need = std::max(need, workspace_bytes_for(di.sms, num_seqs, Hkv, G, cache->head_dim, cache->dtype));
+    *bytes = need;
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
+                                             const int32_t* cu_q, const int32_t* kv_lens, const void* k_cache,
+                                             const void* v_cache, const pkv_cache_desc* cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t num_seqs,
+                                             int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+                                             int32_t* device_error, void* stream) {
+    if (cu_q == nullptr) {  // one query token a sequence: the decode, with the states' lengths as its contexts
+        if (total_q_tokens != num_seqs) {
+            g_detail[0] = 0;
+            return fail(PKV_ERR_INVALID_ARG, "without cu_q total_q_tokens (%d) must be num_seqs (%d)", total_q_tokens,
+                        num_seqs);
+        }
+        return decode_entry(out, q, q_dtype, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, kv_lens,
+                            num_seqs, num_q_heads, scale, 0, 0, workspace, workspace_bytes, device_error, stream, false);
+    }
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (total_q_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (total_q_tokens=%d num_seqs=%d num_q_heads=%d max_blocks_per_seq=%d)",
+                    total_q_tokens, num_seqs, num_q_heads, max_blocks_per_seq);
+    int G;
+    if ((st = check_full("cross attention", q_dtype, *cache, num_q_heads, 128, &G)) != PKV_OK) return st;
+    if (num_seqs > prefill_ws_max_seqs())
+        return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > %d sequences per call", num_seqs, prefill_ws_max_seqs());
+    if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq > INT32_MAX ||
+        static_cast<int64_t>(max_blocks_per_seq) * cache->block_size > INT32_MAX - 64)
+        return fail(PKV_ERR_OUT_OF_RANGE, "block table larger than 2^31-1 entries or 2^31-65 tokens a row");
+    if (!(scale > 0.f && scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and positive");
+    if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
+    if (!out || !q || !kv_lens || !k_cache || !v_cache || !block_tables)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PKV_ERR_INVALID_ARG, "q, out and the caches must be 16-byte aligned");
+    if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_tables))
+        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, 0);
+    if (!workspace || workspace_bytes < fs.total)
+        return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", fs.total,
+                    workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    const int nk = narrow_kind(cache->dtype);
+    if (static_cast<size_t>(di.smem_optin) < prefill_ws_smem_bytes(nk))
+        return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the cross-attention tile");
+    PrefillArgs pa;
+    CUtensorMap qm, km, vm;
+    if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
+                         num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
+        return st;
+    const FullArgs fa = full_args(fs, workspace, total_q_tokens, num_q_heads, false);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention launch");
+    e = launch_full_combine(pa, fa, di.sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention join launch");
     return PKV_OK;
 }

@@ -142,10 +142,48 @@ __device__ __forceinline__ void threads_sync(int nthreads) {
 // WEIGHTED selects this form at compile time.
 constexpr int kCostUnit = 16;  // the weighted split's CTA costs are in 1/16 stream items
 
-template <int G, int S, class KV, int HP, bool WEIGHTED>
+// A batch whose sequences share prefixes (pkv_paged_attention_decode_prefix): the decode streams every sequence's own
+// blocks only and joins its (O, m, l) with the prefix's, which full_tile.cu computed for the whole group and left as
+// records: one row per (sequence, query head) for an item's first piece, 256 rows per CTA of that kernel for the piece
+// its share starts with.
+struct PrefixArgs {
+    const int32_t* cu_groups;    // [num_groups + 1]
+    const int32_t* prefix_lens;  // [num_groups], multiples of S
+    int num_groups;
+    const float* rec_o;          // [rows][128]
+    const float2* rec_ml;        // [rows] (m in log2 units, l)
+    int64_t extra_row;           // the first row of the CTAs' own pieces
+    const int4* seq_plan;        // [B] {stream position of KV head 0's item, key tiles per item, row in the tile, -}
+    const int* share;            // key tiles per CTA of the prefix kernel
+};
+
+// Until the prefix kernel has completed, its results visible (the decode is launched while it runs).
+__device__ __forceinline__ void wait_prefix_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The records of (sequence s, KV head h): piece 0 in the rows of (s, query head), pieces 1 .. n in the rows of CTAs
+// c0 + 1 .. c0 + n, at row_in of their 256.
+struct PrefixPieces {
+    int c0, n, row_in;
+};
+__device__ __forceinline__ PrefixPieces prefix_pieces(const PrefixArgs& px, int s, int h) {
+    const int4 sp = __ldcg(px.seq_plan + s);
+    const int share = __ldcg(px.share);
+    const int U0 = sp.x + h * sp.y, c0 = U0 / share;
+    return {c0, (U0 + sp.y - 1) / share - c0, sp.z};
+}
+// Row of piece k of the (s, query head hq) row, gi being hq's place in its group.
+__device__ __forceinline__ size_t prefix_row(const PrefixArgs& px, const PrefixPieces& pp, int k, int s, int Hq, int hq,
+                                             int gi) {
+    return k == 0 ? static_cast<size_t>(s) * Hq + hq
+                  : static_cast<size_t>(px.extra_row) + static_cast<size_t>(pp.c0 + k) * 256 + pp.row_in + gi;
+}
+
+// PREFIX: the streams hold the sequences' own blocks, off[s] blocks into their tables (-1: a sequence whose length or
+// group is bad; its row is zero); off is in shared memory behind the prefix sums.
+template <int G, int S, class KV, int HP, bool WEIGHTED, bool PREFIX = false>
 __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
                                                 uint8_t* smem_raw, int cta, int ncta, int nthreads,
-                                                const int* pcost, int* cb) {
+                                                const int* pcost, int* cb, const PrefixArgs& px = PrefixArgs{}) {
     constexpr int D = 128;
     constexpr int TS = S < 16 ? S : 16;   // tokens of a block per 16-row MMA tile
     constexpr int NT = S / TS;            // tiles per block
@@ -177,13 +215,31 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         const int s0 = tid * per;
         const int s1 = min(B, s0 + per);
         int local = 0;
+        int grp = 0;
+        if constexpr (PREFIX) {  // the group of this thread's first sequence
+            int hi = px.num_groups - 1;
+            while (grp < hi) {
+                const int mid = (grp + hi + 1) >> 1;
+                if (px.cu_groups[mid] <= s0) grp = mid; else hi = mid - 1;
+            }
+        }
         for (int s = s0; s < s1; ++s) {
             int L = a.context_lens[s];
-            if (L < 0 || L > a.MB * S) {
+            bool bad = L < 0 || L > a.MB * S;
+            int skip = 0;  // blocks of the prefix
+            if constexpr (PREFIX) {
+                while (grp + 1 < px.num_groups && px.cu_groups[grp + 1] <= s) ++grp;
+                const int g0 = px.cu_groups[grp], g1 = px.cu_groups[grp + 1], p = px.prefix_lens[grp];
+                bad = bad || g0 < 0 || g0 > s || g1 <= s || g1 > B || p < 0 || p % S != 0 || p > L;
+                skip = bad ? 0 : p / S;
+                P[B + 1 + s] = bad ? -1 : skip;
+            }
+            if (bad) {
                 if (cta == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
                 L = 0;
             }
-            local += (L + S - 1) / S;
+            local += (L + S - 1) / S - skip;
+            if constexpr (PREFIX) P[s] = (L + S - 1) / S - skip;  // its own blocks, for the second pass
         }
         int incl = local;
 #pragma unroll
@@ -198,10 +254,16 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         for (int i = 0; i < warp; ++i) wbase += warp_tot[i];
         int run = wbase + incl - local;
         for (int s = s0; s < s1; ++s) {
-            P[s] = run;
-            int L = a.context_lens[s];
-            if (L < 0 || L > a.MB * S) L = 0;
-            run += (L + S - 1) / S;
+            if constexpr (PREFIX) {
+                const int n = P[s];
+                P[s] = run;
+                run += n;
+            } else {
+                P[s] = run;
+                int L = a.context_lens[s];
+                if (L < 0 || L > a.MB * S) L = 0;
+                run += (L + S - 1) / S;
+            }
         }
         if (tid == nthreads - 1) {
             int tot = 0;
@@ -210,10 +272,12 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         }
         threads_sync(nthreads);
     }
+    const int* off = P + B + 1;  // PREFIX
 
     // ---- 2. empty sequences get zero rows (spread over the CTAs)
     for (int s = cta; s < B; s += ncta) {
         if (P[s + 1] != P[s]) continue;
+        if (PREFIX && off[s] > 0) continue;  // the prefix alone: the kernel's last step
         const int n = a.Hq * D;
         for (int i = tid; i < n; i += nthreads) reinterpret_cast<uint16_t*>(a.out)[static_cast<size_t>(s) * n + i] = 0;
     }
@@ -331,9 +395,10 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         const int u = local / nb;
         const int j = local - u * nb;
         const int L = a.context_lens[s];
+        const int jt = PREFIX ? off[s] + j : j;  // its place in the table
         m.a = s * 1024 + u;
-        m.b = a.block_tables[static_cast<size_t>(s) * a.MB + j];
-        const int valid = min(S, L - j * S);
+        m.b = a.block_tables[static_cast<size_t>(s) * a.MB + jt];
+        const int valid = min(S, L - jt * S);
         m.c = valid | (j == 0 ? kMetaFirst : 0) | (j == nb - 1 ? kMetaLast : 0) |
               ((m.b >= 0 && m.b < a.NB) ? kMetaOk : 0);
         return m;
@@ -525,6 +590,20 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         }
         // out[s][query head u GU + r_row][d0 .. d0 + DPL), bf16
         const int hh = r_row / G;
+        if constexpr (PREFIX) {
+            if (off[s] > 0) {
+                wait_prefix_kernel();
+                const PrefixPieces pp = prefix_pieces(px, s, u * HP + hh);
+                for (int k = 0; k <= pp.n; ++k) {
+                    const size_t row = prefix_row(px, pp, k, s, a.Hq, u * GU + r_row, r_row % G);
+                    const float2 ml = __ldcg(px.rec_ml + row);
+                    float4 ov[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) ov[i] = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * D + d0) + i);
+                    combine(ml.x, ml.y, ov);
+                }
+            }
+        }
         const float inv = Ls > 0.f ? out_mul(u, hh) / Ls : 0.f;
         uint8_t* orow = reinterpret_cast<uint8_t*>(a.out) +
                         (static_cast<size_t>(s) * a.Hq + static_cast<size_t>(u) * GU + r_row) * D * 2 + d0 * 2;
@@ -826,7 +905,32 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
                 for (int hh = 0; hh < HP; ++hh) {
                     float v[32];
                     o_row(o, hh, v);
-                    store_row(s, u, hh, v, l_run[hh] > 0.f ? out_mul(u, hh) / l_run[hh] : 0.f);
+                    float l = l_run[hh];
+                    if constexpr (PREFIX) {
+                        if (off[s] > 0) {
+                            wait_prefix_kernel();
+                            const PrefixPieces pp = prefix_pieces(px, s, u * HP + hh);
+                            float m = m_ref[hh];
+                            for (int k = 0; k <= pp.n; ++k) {
+                                const size_t row = prefix_row(px, pp, k, s, a.Hq, (u * HP + hh) * G + g, g);
+                                const float2 ml = __ldcg(px.rec_ml + row);
+                                const float mn = fmaxf(m, ml.x);
+                                const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                                const float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+                                l = l * w0 + ml.y * w1;
+                                m = mn;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 x = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * D + dim_of(4 * i)));
+                                    v[4 * i] = v[4 * i] * w0 + x.x * w1;
+                                    v[4 * i + 1] = v[4 * i + 1] * w0 + x.y * w1;
+                                    v[4 * i + 2] = v[4 * i + 2] * w0 + x.z * w1;
+                                    v[4 * i + 3] = v[4 * i + 3] * w0 + x.w * w1;
+                                }
+                            }
+                        }
+                    }
+                    store_row(s, u, hh, v, l > 0.f ? out_mul(u, hh) / l : 0.f);
                 }
             }
             resolve_pending();
@@ -879,6 +983,62 @@ __global__ void __launch_bounds__(32 * kMmaWarps, 1)
     extern __shared__ uint8_t smem_raw[];
     decode_mma_body<G, S, KV, HP, false>(kmap, vmap, a, smem_raw, blockIdx.x, gridDim.x, blockDim.x, nullptr,
                                          nullptr);
+}
+
+// The decode of sequences that share prefixes (decode_prefix_*.cu), launched while the prefix kernel runs.
+template <int G, int S, class KV, int HP>
+__global__ void __launch_bounds__(32 * kMmaWarps, 1)
+    paged_decode_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                               const DecodeArgs a, const PrefixArgs px) {
+    extern __shared__ uint8_t smem_raw[];
+    decode_mma_body<G, S, KV, HP, false, true>(kmap, vmap, a, smem_raw, blockIdx.x, gridDim.x, blockDim.x, nullptr,
+                                               nullptr, px);
+    wait_prefix_kernel();  // in every warp: this kernel does not end before the prefix kernel
+    // sequences that are their prefix and nothing more: a warp per sequence, four head dims per lane
+    const int* P = reinterpret_cast<const int*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    for (int s = blockIdx.x * nw + warp; s < a.B; s += gridDim.x * nw) {
+        if (P[s + 1] != P[s] || P[a.B + 1 + s] <= 0) continue;
+        for (int hq = 0; hq < a.Hq; ++hq) {
+            const PrefixPieces pp = prefix_pieces(px, s, hq / G);
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k <= pp.n; ++k) {
+                const size_t row = prefix_row(px, pp, k, s, a.Hq, hq, hq % G);
+                const float2 ml = __ldcg(px.rec_ml + row);
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * 128) + lane);
+                const float mn = fmaxf(m, ml.x);
+                const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                const float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+                l = l * w0 + ml.y * w1;
+                m = mn;
+                o = make_float4(o.x * w0 + x.x * w1, o.y * w0 + x.y * w1, o.z * w0 + x.z * w1, o.w * w0 + x.w * w1);
+            }
+            const float mul = a.v_head ? __ldg(a.v_head + hq / G) : a.o_mul;
+            const float inv = l > 0.f ? mul / l : 0.f;
+            reinterpret_cast<uint2*>(a.out)[(static_cast<size_t>(s) * a.Hq + hq) * 32 + lane] =
+                make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv));
+        }
+    }
+}
+
+template <int G, int S, class KV, int HP>
+cudaError_t launch_paged_decode_prefix(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
+                                       const PrefixArgs& px, int grid, int block, size_t smem, cudaStream_t stream) {
+    auto kern = paged_decode_prefix_kernel<G, S, KV, HP>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, px);
 }
 
 // Host-side launch for one instantiation (defined in decode_mma_*.cu).
