@@ -1073,7 +1073,7 @@ PKV_API pkv_status pkv_extend_sequences(int32_t* block_tables, int32_t max_block
     if ((st = device_info(&di)) != PKV_OK) return st;
     ExtendArgs a{block_tables, past_lens, new_lens, free_blocks, free_count, seq_lens, new_free_count, cu_q, q_starts,
                  slot_mapping, device_error, num_seqs, max_blocks_per_seq, log2_of(block_size), num_blocks, max_tokens};
-    const cudaError_t e = launch_extend_sequences(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_extend_sequences(a, di.sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "extend_sequences launch");
     return PKV_OK;
 }
@@ -1096,7 +1096,7 @@ PKV_API pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t ma
     if ((st = device_info(&di)) != PKV_OK) return st;
     ReleaseArgs a{block_tables, past_lens, finished, keep_blocks, free_blocks, free_count, seq_lens, new_free_count,
                   device_error, num_seqs, max_blocks_per_seq, log2_of(block_size), num_blocks};
-    const cudaError_t e = launch_release_sequences(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_release_sequences(a, di.sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "release_sequences launch");
     return PKV_OK;
 }

@@ -8,10 +8,10 @@
 // would give, known for every block at once.  Releasing is the mirror image: block i of the finished sequence s goes to
 // free[F + E_s + i].
 //
-// The work is a scan over the batch and then independent writes, so a call is bound by latency until its writes fill
-// some SMs.  One CTA, or for many writes one cluster of CTAs, runs the whole call: every CTA scans the whole batch for
-// itself (at most 8 sequences a thread), keeps the sums in shared memory and writes its part; the cluster barrier,
-// which every CTA passes only after its last read of the lengths, lets the first CTA then write them in place.
+// The work is a scan over the batch and then independent writes.  Every CTA scans the whole batch for itself (at most 8
+// sequences a thread), keeps the sums in shared memory and writes its part, so one launch does the call without the CTAs
+// having to wait for one another.  Lengths and the free count may be updated in place, which nobody may do while a CTA
+// still reads them: with one CTA it is the last thing it does, with several a second small kernel does it after them.
 #include <algorithm>
 
 #include "tables.cuh"
@@ -19,21 +19,6 @@
 namespace pkv {
 
 namespace {
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Block-wide exclusive sums of two values per thread (the first in 64 bits); returns the totals in ta, tb.
 __device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t& ta, int& tb, int64_t* wa, int* wb) {
@@ -87,18 +72,15 @@ constexpr int kRun = 4;  // consecutive items per thread: one search serves them
 
 }  // namespace
 
-__global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs a) {
-    extern __shared__ int smem[];
+// The scan of an extend step; the sums before each sequence go to tok and blk ([N + 1]) when the step is possible.
+struct ExtendScan {
+    int F, T, E;  // free blocks before the step, its tokens and its blocks (0 for a refused step)
+    bool ok;
+};
+__device__ __forceinline__ ExtendScan scan_extend(const ExtendArgs& a, int* tok, int* blk, int* past, bool report) {
     __shared__ int64_t wa[32];
     __shared__ int wb[32];
-    int* tok = smem;              // [N + 1] exclusive sums of the new tokens
-    int* blk = tok + a.N + 1;     // [N + 1] exclusive sums of the new blocks
-    int* past = blk + a.N + 1;    // [N]
-    const int tid = threadIdx.x, N = a.N, S = 1 << a.shift, mask = S - 1;
-    const uint32_t rank = cluster_rank();
-    const int width = static_cast<int>(cluster_size() * blockDim.x), at = static_cast<int>(rank * blockDim.x) + tid;
-
-    // ---- the scan: new tokens and new blocks before each sequence
+    const int tid = threadIdx.x, N = a.N, mask = (1 << a.shift) - 1;
     const int per = (N + blockDim.x - 1) / blockDim.x;
     const int lo = min(tid * per, N), hi = min(lo + per, N);
     const int F = *a.free_count;
@@ -112,9 +94,12 @@ __global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs
             bad = true;
             continue;
         }
+        const int e = ((L + n + mask) >> a.shift) - ((L + mask) >> a.shift);
         past[s] = L;
+        tok[s] = n;
+        blk[s] = e;
         nt += n;
-        nb += ((L + n + mask) >> a.shift) - ((L + mask) >> a.shift);
+        nb += e;
     }
     int64_t total_t;
     int total_b;
@@ -124,24 +109,43 @@ __global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs
     const bool ok = !bad && !no_room && total_t <= a.max_tokens;
     if (ok) {
         for (int s = lo; s < hi; ++s) {
-            const int L = past[s], n = a.new_lens[s];
+            const int n = tok[s], e = blk[s];
             tok[s] = static_cast<int>(nt);
             blk[s] = nb;
             nt += n;
-            nb += ((L + n + mask) >> a.shift) - ((L + mask) >> a.shift);
+            nb += e;
         }
         if (tid == 0) {
             tok[N] = static_cast<int>(total_t);
             blk[N] = total_b;
         }
-    } else if (rank == 0 && tid == 0) {
+    } else if (report && tid == 0) {
         raise_error(a.err, (bad || total_t > a.max_tokens ? PKV_DEVERR_BAD_LENGTH : 0) | (no_room ? PKV_DEVERR_BAD_SLOT : 0));
     }
     __syncthreads();
+    return {F, ok ? static_cast<int>(total_t) : 0, ok ? total_b : 0, ok};
+}
+
+// The lengths and the free count after the step, in place perhaps: for a CTA after which nobody reads the old ones.
+__device__ __forceinline__ void write_extend_state(const ExtendArgs& a, const ExtendScan& r, const int* tok, const int* past) {
+    for (int s = threadIdx.x; s < a.N; s += blockDim.x)
+        a.seq_lens[s] = r.ok ? past[s] + (tok[s + 1] - tok[s]) : a.past_lens[s];  // a refused step leaves them
+    if (threadIdx.x == 0) *a.new_free_count = r.F - r.E;
+}
+
+__global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs a, bool write_state) {
+    extern __shared__ int smem[];
+    int* tok = smem;              // [N + 1] exclusive sums of the new tokens
+    int* blk = tok + a.N + 1;     // [N + 1] exclusive sums of the new blocks
+    int* past = blk + a.N + 1;    // [N]
+    const int tid = threadIdx.x, N = a.N, mask = (1 << a.shift) - 1;
+    const int width = static_cast<int>(gridDim.x * blockDim.x), at = static_cast<int>(blockIdx.x * blockDim.x) + tid;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const ExtendScan r = scan_extend(a, tok, blk, past, blockIdx.x == 0);
+    const int F = r.F, T = r.T, E = r.E;
 
     // ---- the new blocks' table entries and the new tokens' slots.  A refused step has neither: every slot is -1.
-    const int T = ok ? static_cast<int>(total_t) : 0, E = ok ? total_b : 0;
-    auto free_id = [&](int e) {  // the e-th block taken by the step; -1 (and an error) if the stack's entry is no block
+    auto free_id = [&](int e) {  // the e-th block taken by the step; -1 if the stack's entry is no block
         const int id = __ldg(a.free_blocks + (F - 1 - e));
         return id >= 0 && id < a.NB ? id : -1;
     };
@@ -189,125 +193,152 @@ __global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs
         }
     }
 
-    // ---- the state, which may be the input arrays: written once no CTA reads them any more
-    cluster_arrive();
-    cluster_wait();
-    if (rank != 0) return;
-    for (int s = tid; s < N; s += blockDim.x) {
-        const int L = ok ? past[s] : a.past_lens[s];  // a refused step leaves the lengths as they are
-        if (a.q_starts) a.q_starts[s] = L;
-        if (a.cu_q) a.cu_q[s] = ok ? tok[s] : 0;
-        a.seq_lens[s] = ok ? L + (tok[s + 1] - tok[s]) : L;
+    // ---- the step's index arrays, and its state
+    for (int s = at; s <= N; s += width) {
+        if (a.cu_q) a.cu_q[s] = r.ok ? tok[s] : 0;
+        if (a.q_starts && s < N) a.q_starts[s] = r.ok ? past[s] : a.past_lens[s];
     }
-    if (tid == 0) {
-        if (a.cu_q) a.cu_q[N] = T;
-        *a.new_free_count = F - E;
-    }
+    if (write_state && blockIdx.x == 0) write_extend_state(a, r, tok, past);
 }
 
-__global__ void __launch_bounds__(1024) release_sequences_kernel(const ReleaseArgs a) {
+// In place, after every CTA of extend_sequences_kernel.
+__global__ void __launch_bounds__(1024) extend_state_kernel(const ExtendArgs a) {
     extern __shared__ int smem[];
+    int* tok = smem;
+    int* past = tok + 2 * (a.N + 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ExtendScan r = scan_extend(a, tok, tok + a.N + 1, past, false);
+    write_extend_state(a, r, tok, past);
+}
+
+// The scan of a release; the sums before each sequence go to blk ([N + 1]), the lengths after it to len ([N]).
+struct ReleaseScan {
+    int F, E;
+    bool ok;
+};
+__device__ __forceinline__ ReleaseScan scan_release(const ReleaseArgs& a, int* blk, int* len, bool report) {
     __shared__ int64_t wa[32];
     __shared__ int wb[32];
-    int* blk = smem;            // [N + 1] exclusive sums of the released blocks
-    int* len = blk + a.N + 1;   // [N] the lengths after the call
     const int tid = threadIdx.x, N = a.N, mask = (1 << a.shift) - 1;
-    const uint32_t rank = cluster_rank();
-    const int width = static_cast<int>(cluster_size() * blockDim.x), at = static_cast<int>(rank * blockDim.x) + tid;
-
     const int per = (N + blockDim.x - 1) / blockDim.x;
     const int lo = min(tid * per, N), hi = min(lo + per, N);
     const int F = *a.free_count;
     const int64_t cap = static_cast<int64_t>(a.MB) << a.shift;
-    auto count = [&](int s, bool& bad) {  // blocks that sequence s hands back
-        const int L = a.past_lens[s], k = a.keep_blocks ? a.keep_blocks[s] : 0;
-        if (L < 0 || L > cap || k < 0) {
-            bad = true;
-            return 0;
-        }
-        len[s] = a.finished[s] ? 0 : L;
-        return a.finished[s] ? max(0, ((L + mask) >> a.shift) - k) : 0;
-    };
-    int64_t n64 = 0;
+    int64_t n = 0;
     int none = 0;
     bool bad = false;
-    for (int s = lo; s < hi; ++s) n64 += count(s, bad);
+    for (int s = lo; s < hi; ++s) {
+        const int L = a.past_lens[s], k = a.keep_blocks ? a.keep_blocks[s] : 0;
+        const bool done = a.finished[s] != 0;
+        if (L < 0 || L > cap || k < 0) {
+            bad = true;
+            continue;
+        }
+        len[s] = done ? 0 : L;
+        blk[s] = done ? max(0, ((L + mask) >> a.shift) - k) : 0;
+        n += blk[s];
+    }
     int64_t total;
     int zero;
-    block_scan2(n64, none, total, zero, wa, wb);
+    block_scan2(n, none, total, zero, wa, wb);
     bad = __syncthreads_or(bad);
     const bool no_room = F < 0 || F > a.NB || total > a.NB - F;
     const bool ok = !bad && !no_room;
     if (ok) {
         for (int s = lo; s < hi; ++s) {
-            blk[s] = static_cast<int>(n64);
-            n64 += count(s, bad);
+            const int e = blk[s];
+            blk[s] = static_cast<int>(n);
+            n += e;
         }
         if (tid == 0) blk[N] = static_cast<int>(total);
-    } else if (rank == 0 && tid == 0) {
+    } else if (report && tid == 0) {
         raise_error(a.err, (bad ? PKV_DEVERR_BAD_LENGTH : 0) | (no_room ? PKV_DEVERR_BAD_SLOT : 0));
     }
     __syncthreads();
-    const int E = ok ? static_cast<int>(total) : 0;
-    for (int64_t i = static_cast<int64_t>(at) * kRun; i < E; i += static_cast<int64_t>(width) * kRun) {
-        int s = find_run(blk, N, static_cast<int>(i));
-#pragma unroll
-        for (int u = 0; u < kRun; ++u) {
-            const int e = static_cast<int>(i) + u;
-            if (e >= E) break;
-            while (blk[s + 1] <= e) ++s;  // blk[N] = E > e
-            const int k = a.keep_blocks ? a.keep_blocks[s] : 0;
-            int id = a.tables[static_cast<size_t>(s) * a.MB + k + (e - blk[s])];
-            if (id < 0 || id >= a.NB) {
-                id = -1;
-                raise_error(a.err, PKV_DEVERR_BAD_BLOCK);
-            }
-            a.free_blocks[F + e] = id;
+    return {F, ok ? static_cast<int>(total) : 0, ok};
+}
+
+__device__ __forceinline__ void write_release_state(const ReleaseArgs& a, const ReleaseScan& r, const int* len) {
+    for (int s = threadIdx.x; s < a.N; s += blockDim.x) a.seq_lens[s] = r.ok ? len[s] : a.past_lens[s];
+    if (threadIdx.x == 0) *a.new_free_count = r.F + r.E;
+}
+
+__global__ void __launch_bounds__(1024) release_sequences_kernel(const ReleaseArgs a, bool write_state) {
+    extern __shared__ int smem[];
+    int* blk = smem;
+    int* len = blk + a.N + 1;
+    const int width = static_cast<int>(gridDim.x * blockDim.x), at = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const ReleaseScan r = scan_release(a, blk, len, blockIdx.x == 0);
+    for (int e = at; e < r.E; e += width) {
+        const int s = find_run(blk, a.N, e);
+        const int k = a.keep_blocks ? __ldg(a.keep_blocks + s) : 0;
+        int id = __ldg(a.tables + static_cast<size_t>(s) * a.MB + k + (e - blk[s]));
+        if (id < 0 || id >= a.NB) {
+            id = -1;
+            raise_error(a.err, PKV_DEVERR_BAD_BLOCK);
         }
+        a.free_blocks[r.F + e] = id;
     }
-    cluster_arrive();
-    cluster_wait();
-    if (rank != 0) return;
-    for (int s = tid; s < N; s += blockDim.x) a.seq_lens[s] = ok ? len[s] : a.past_lens[s];
-    if (tid == 0) *a.new_free_count = F + E;
+    if (write_state && blockIdx.x == 0) write_release_state(a, r, len);
+}
+
+// In place, after every CTA of release_sequences_kernel.
+__global__ void __launch_bounds__(1024) release_state_kernel(const ReleaseArgs a) {
+    extern __shared__ int smem[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ReleaseScan r = scan_release(a, smem, smem + a.N + 1, false);
+    write_release_state(a, r, smem + a.N + 1);
 }
 
 namespace {
 
-// One CTA for a step of few writes; one cluster of kCluster CTAs for more.  A CTA of 1024 threads writes kSingle items
-// about as fast as the cluster starts up and synchronises.
-constexpr int kCluster = 8;
-constexpr int64_t kSingle = 8192;
+// A call of up to kSingle items (slots, or table entries) is one CTA: it ends as soon as several would.
+constexpr int64_t kSingle = 4096;
 
-template <class Kernel, class Args>
-cudaError_t launch(Kernel kern, const Args& a, int64_t items, size_t smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+// The kernel over as many CTAs as its items fill, and behind it the state kernel when the state is updated in place and
+// there is more than one CTA to read it.
+template <class Kernel, class State, class Args>
+cudaError_t launch(Kernel kern, State state, const Args& a, bool in_place, int64_t items, size_t smem, int sms,
+                   cudaStream_t stream) {
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    const int grid = items <= kSingle ? 1 : static_cast<int>(std::min<int64_t>(sms, (items + kSingle - 1) / kSingle));
+    const int block = a.N <= 256 && items <= 1024 ? 256 : 1024;
+    const bool second = in_place && grid > 1;
+    kern<<<grid, block, smem, stream>>>(a, !second);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !second) return e;
     cudaLaunchConfig_t cfg = {};
-    const int ncta = items > kSingle ? kCluster : 1;
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(a.N <= 256 && items <= 1024 ? 256 : 1024);
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ncta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, state, a);
 }
 
 }  // namespace
 
-cudaError_t launch_extend_sequences(const ExtendArgs& a, cudaStream_t stream) {
+cudaError_t launch_extend_sequences(const ExtendArgs& a, int sms, cudaStream_t stream) {
     const size_t smem = (3 * static_cast<size_t>(a.N) + 2) * 4;
-    return launch(extend_sequences_kernel, a, a.max_tokens, smem, stream);
+    const bool in_place = a.seq_lens == a.past_lens || a.new_free_count == a.free_count;
+    return launch(extend_sequences_kernel, extend_state_kernel, a, in_place, a.max_tokens, smem, sms, stream);
 }
 
-cudaError_t launch_release_sequences(const ReleaseArgs& a, cudaStream_t stream) {
+cudaError_t launch_release_sequences(const ReleaseArgs& a, int sms, cudaStream_t stream) {
     const size_t smem = (2 * static_cast<size_t>(a.N) + 1) * 4;
-    return launch(release_sequences_kernel, a, static_cast<int64_t>(a.N) * a.MB, smem, stream);
+    const bool in_place = a.seq_lens == a.past_lens || a.new_free_count == a.free_count;
+    return launch(release_sequences_kernel, release_state_kernel, a, in_place, static_cast<int64_t>(a.N) * a.MB, smem, sms,
+                  stream);
 }
 
 }  // namespace pkv

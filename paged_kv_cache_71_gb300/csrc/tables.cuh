@@ -35,7 +35,7 @@ struct ReleaseArgs {
 
 constexpr int kMaxTableSeqs = 8192;
 
-cudaError_t launch_extend_sequences(const ExtendArgs& a, cudaStream_t stream);
-cudaError_t launch_release_sequences(const ReleaseArgs& a, cudaStream_t stream);
+cudaError_t launch_extend_sequences(const ExtendArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_release_sequences(const ReleaseArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace pkv
