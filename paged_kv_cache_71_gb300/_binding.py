@@ -125,7 +125,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -258,23 +258,23 @@ def pkv_block_hashes(token_ids, cu_tokens, block_size: int, out_offsets, hashes,
            "pkv_block_hashes")
 
 
-def _expect(func: str, *wanted) -> None:
-    """Refuse tensors that the pointers alone would not tell from good ones.  Each of `wanted` is (name, tensor, dtypes,
-    shape); layouts must be contiguous, and every tensor on the current CUDA device."""
+def _expect(func: str, names: str, *wanted) -> None:
+    """Refuse tensors that the pointers alone would not tell from good ones.  Each of `wanted` is (tensor, dtypes, shape);
+    layouts must be contiguous, and every tensor on the current CUDA device."""
     device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    for _, t, dtypes, shape in wanted:
+    for t, dtypes, shape in wanted:
         if not (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device >= 0):
             break
     else:
         return
-    for name, t, dtypes, shape in wanted:  # something is wrong: say what
+    for name, (t, dtypes, shape) in zip(names.split(), wanted):  # something is wrong: say what
         if t.dtype not in dtypes:
             raise PkvError(1, func, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
         if t.shape != shape:
             raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise PkvError(1, func, f"{name} must be contiguous")
-    for name, t, _, _ in wanted:
+    for name, (t, _, _) in zip(names.split(), wanted):
         if device < 0 or t.get_device() != device:
             raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
 
@@ -289,13 +289,14 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
     """Block tables, lengths and slot map of a step from the request lengths, on the GPU.  seq_lens may be past_lens and
     new_free_count may be free_count (in place); free_blocks has one entry per block of the pool."""
     L, n = lib(), past_lens.shape[0]
-    _expect("pkv_extend_sequences", ("block_tables", block_tables, _I32, (n, block_tables.shape[-1])),
-            ("past_lens", past_lens, _I32, (n,)), ("new_lens", new_lens, _I32, (n,)),
-            ("free_blocks", free_blocks, _I32, (free_blocks.numel(),)), ("free_count", free_count, _I32, (1,)),
-            ("seq_lens", seq_lens, _I32, (n,)), ("new_free_count", new_free_count, _I32, (1,)),
-            ("slot_mapping", slot_mapping, _I64, (slot_mapping.numel(),)),
-            *((("cu_q", cu_q, _I32, (n + 1,)),) if cu_q is not None else ()),
-            *((("q_starts", q_starts, _I32, (n,)),) if q_starts is not None else ()))
+    seqs = (n,)
+    _expect("pkv_extend_sequences",
+            "block_tables past_lens new_lens free_blocks free_count seq_lens new_free_count slot_mapping q_starts cu_q",
+            (block_tables, _I32, (n, block_tables.shape[-1])), (past_lens, _I32, seqs), (new_lens, _I32, seqs),
+            (free_blocks, _I32, (free_blocks.numel(),)), (free_count, _I32, (1,)), (seq_lens, _I32, seqs),
+            (new_free_count, _I32, (1,)), (slot_mapping, _I64, (slot_mapping.numel(),)),
+            (past_lens if q_starts is None else q_starts, _I32, seqs),
+            (free_count, _I32, (1,)) if cu_q is None else (cu_q, _I32, (n + 1,)))
     _check(L.pkv_extend_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(new_lens), n,
                                   int(block_size), _ptr(free_blocks), _ptr(free_count), free_blocks.shape[0],
                                   _ptr(seq_lens), _ptr(new_free_count), _ptr(slot_mapping), slot_mapping.shape[0],
@@ -307,11 +308,12 @@ def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, fr
                           new_free_count, keep_blocks=None, device_error=None, stream=None) -> None:
     """Finished sequences hand their blocks back to the free stack, on the GPU (finished: bool or uint8 [num_seqs])."""
     L, n = lib(), past_lens.shape[0]
-    _expect("pkv_release_sequences", ("block_tables", block_tables, _I32, (n, block_tables.shape[-1])),
-            ("past_lens", past_lens, _I32, (n,)), ("finished", finished, _FLAG, (n,)),
-            ("free_blocks", free_blocks, _I32, (free_blocks.numel(),)), ("free_count", free_count, _I32, (1,)),
-            ("seq_lens", seq_lens, _I32, (n,)), ("new_free_count", new_free_count, _I32, (1,)),
-            *((("keep_blocks", keep_blocks, _I32, (n,)),) if keep_blocks is not None else ()))
+    seqs = (n,)
+    _expect("pkv_release_sequences",
+            "block_tables past_lens finished free_blocks free_count seq_lens new_free_count keep_blocks",
+            (block_tables, _I32, (n, block_tables.shape[-1])), (past_lens, _I32, seqs), (finished, _FLAG, seqs),
+            (free_blocks, _I32, (free_blocks.numel(),)), (free_count, _I32, (1,)), (seq_lens, _I32, seqs),
+            (new_free_count, _I32, (1,)), (past_lens if keep_blocks is None else keep_blocks, _I32, seqs))
     _check(L.pkv_release_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(finished),
                                    _ptr(keep_blocks), n, int(block_size), _ptr(free_blocks), _ptr(free_count),
                                    free_blocks.shape[0], _ptr(seq_lens), _ptr(new_free_count), _ptr(device_error),
@@ -335,12 +337,11 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
     L, (n, heads, D) = lib(), q.shape
     caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
     groups = prefix_lens.shape[0]
-    _expect("pkv_paged_attention_decode_prefix", ("q", q, _FLOATS, (n, heads, cache.head_dim)),
-            ("out", out, (q.dtype,), (n, heads, D)), ("k_cache", k_cache, _CACHES, caches),
-            ("v_cache", v_cache, (k_cache.dtype,), caches),
-            ("block_tables", block_tables, _I32, (n, block_tables.shape[-1])),
-            ("context_lens", context_lens, _I32, (n,)), ("cu_groups", cu_groups, _I32, (groups + 1,)),
-            ("prefix_lens", prefix_lens, _I32, (groups,)))
+    _expect("pkv_paged_attention_decode_prefix",
+            "q out k_cache v_cache block_tables context_lens cu_groups prefix_lens",
+            (q, _FLOATS, (n, heads, cache.head_dim)), (out, (q.dtype,), (n, heads, D)), (k_cache, _CACHES, caches),
+            (v_cache, (k_cache.dtype,), caches), (block_tables, _I32, (n, block_tables.shape[-1])),
+            (context_lens, _I32, (n,)), (cu_groups, _I32, (groups + 1,)), (prefix_lens, _I32, (groups,)))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(L.pkv_paged_attention_decode_prefix(_ptr(out), _ptr(q), _dtype(q), _ptr(k_cache), _ptr(v_cache),
                                                ctypes.byref(cache), _ptr(block_tables), block_tables.shape[1],
@@ -365,11 +366,11 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
     [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
     L, (tokens, heads, D), n = lib(), q.shape, kv_lens.shape[0]
     caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
-    _expect("pkv_paged_cross_attention", ("q", q, _FLOATS, (tokens, heads, cache.head_dim)),
-            ("out", out, (q.dtype,), (tokens, heads, D)), ("kv_lens", kv_lens, _I32, (n,)),
-            ("k_cache", k_cache, _CACHES, caches), ("v_cache", v_cache, (k_cache.dtype,), caches),
-            ("block_tables", block_tables, _I32, (n, block_tables.shape[-1])),
-            *((("cu_q", cu_q, _I32, (n + 1,)),) if cu_q is not None else ()))
+    _expect("pkv_paged_cross_attention", "q out kv_lens k_cache v_cache block_tables cu_q",
+            (q, _FLOATS, (tokens, heads, cache.head_dim)), (out, (q.dtype,), (tokens, heads, D)), (kv_lens, _I32, (n,)),
+            (k_cache, _CACHES, caches), (v_cache, (k_cache.dtype,), caches),
+            (block_tables, _I32, (n, block_tables.shape[-1])),
+            (kv_lens, _I32, (n,)) if cu_q is None else (cu_q, _I32, (n + 1,)))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(L.pkv_paged_cross_attention(_ptr(out), _ptr(q), _dtype(q), tokens, _ptr(cu_q), _ptr(kv_lens),
                                        _ptr(k_cache), _ptr(v_cache), ctypes.byref(cache), _ptr(block_tables),

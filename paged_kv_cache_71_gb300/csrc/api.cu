@@ -1117,12 +1117,12 @@ static FullScratch full_scratch(int sms, int tokens, int Hq, int plan_seqs) {
     f.plan = f.share + 256;
     f.ml = f.plan + up(static_cast<size_t>(plan_seqs) * 16);
     f.o = f.ml + up(rows * 8);
-    f.total = f.o + rows * 512;
+    f.total = f.o + rows * 512 + 256;  // the caller's base may be aligned to 16 bytes only
     return f;
 }
 
 static FullArgs full_args(const FullScratch& f, void* base, int tokens, int Hq, bool prefix) {
-    uint8_t* p = static_cast<uint8_t*>(base);
+    uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
     FullArgs a;
     a.rec_o = reinterpret_cast<float*>(p + f.o);
     a.rec_ml = reinterpret_cast<float2*>(p + f.ml);
@@ -1299,7 +1299,7 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
     if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     const bool b16 = cache->dtype == PKV_BF16, nar = narrow(cache->dtype);
     const int nk = narrow_kind(cache->dtype);
-    if (static_cast<size_t>(di.smem_optin) < prefill_ws_smem_bytes(nk))
+    if (static_cast<size_t>(di.smem_optin) < paged_full_smem_bytes(nk))
         return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the prefix tile");
 
     // ---- the prefixes, each for its whole group
@@ -1447,7 +1447,7 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
                     workspace ? workspace_bytes : static_cast<size_t>(0));
     if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     const int nk = narrow_kind(cache->dtype);
-    if (static_cast<size_t>(di.smem_optin) < prefill_ws_smem_bytes(nk))
+    if (static_cast<size_t>(di.smem_optin) < paged_full_smem_bytes(nk))
         return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the cross-attention tile");
     PrefillArgs pa;
     CUtensorMap qm, km, vm;

@@ -14,7 +14,7 @@ struct FullArgs {
     int64_t extra_row;   // first row of the CTAs' own pieces: total_q_tokens * Hq
     int4* cuts;          // [CTAs] the item that CTA c's share starts inside of (CutItem)
     int4* seq_plan;      // prefix form: [num_seqs] (SeqPlan), else nullptr
-    int* share;          // key tiles per CTA (prefix form reads it)
+    int* share;          // key tiles per CTA
     bool prefix;         // chunks are groups: chunk g's table row is that of its first token (sequence)
 };
 
@@ -22,6 +22,7 @@ struct FullArgs {
 // whose key tiles are stream positions [U0, U1); U1 = 0: it does not.
 // seq_plan[s] = {U0 of the tile's head 0, key tiles per item, row of the sequence's first query head in its tile, 0}.
 
+size_t paged_full_smem_bytes(int narrow);
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const PrefillArgs& a, const FullArgs& f, int narrow, int grid, cudaStream_t stream);
 cudaError_t launch_full_combine(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream);

@@ -24,20 +24,6 @@ struct PrefillArgs {
     uint64_t timeout_ns;
 };
 
-// One run of key tiles of a pair of query tiles without a causal mask (full_tile.cu): key tiles [j0, j0 + n_tiles) of
-// the chunk's kv_len keys, query tokens [i0, i0 + 2 * 128 / G) of the chunk's NQ (the first at row q_base of q).
-struct FullJob {
-    int q_base = 0, NQ = 0, i0 = 0;
-    int kv_len = 0;
-    const int32_t* table = nullptr;
-    int j0 = 0, n_tiles = 0;
-    // nullptr: the result goes to out.  Else a partial record: unnormalised O [row][128] and (m, l) [row], the rows
-    // indexed by (token, query head) or by the tile pair's own 256 rows.
-    float* rec_o = nullptr;
-    float2* rec_ml = nullptr;
-    bool rec_by_token = false;
-};
-
 size_t prefill_ws_smem_bytes(int narrow);
 int prefill_ws_max_seqs();
 

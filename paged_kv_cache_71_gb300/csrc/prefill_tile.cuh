@@ -203,12 +203,9 @@ __device__ __forceinline__ uint32_t s8x2_to_f16x2(uint32_t f, int i0) {
 // (of grid_x slots; the varlen form maps slots to chunks) of KV head h, with the CTA's dynamic shared memory at
 // smem_raw.  ADAPT (INT8 caches, varlen launches): each CTA chooses split widening when only its query tile A is
 // live.  REUSE: the CTA goes on to other work afterwards, so the tile's mbarriers are invalidated before it returns.
-// FULL: no causal mask and an explicit job (FullJob) instead of a slot: a run of key tiles of a pair of query tiles,
-// whose result goes out as it is or as a partial (O, m, l) record.
-template <int NARROW, bool ADAPT, bool REUSE, bool FULL = false>
+template <int NARROW, bool ADAPT, bool REUSE>
 __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                             const PrefillArgs& a, int tile_x, int h, int grid_x, uint8_t* smem_raw,
-                                             const FullJob& job = FullJob{}) {
+                                             const PrefillArgs& a, int tile_x, int h, int grid_x, uint8_t* smem_raw) {
     constexpr int kStages = Plan<NARROW>::kStages, kOffK = Plan<NARROW>::kOffK, kOffV = Plan<NARROW>::kOffV;
     constexpr int kOffStg = Plan<NARROW>::kOffStg, kOffMeta = Plan<NARROW>::kOffMeta, kStage = Plan<NARROW>::kStage;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -225,9 +222,8 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
     int* tcount = reinterpret_cast<int*>(smem + kOffMeta + kMetaCount);
 
     // ---- which chunk and which tokens: chunk s covers CTAs [tcount[s], tcount[s+1]) of the grid
-    const bool single = !FULL && a.cu_q == nullptr;  // one chunk described by the scalar fields
-    if constexpr (FULL) {
-    } else if (single) {
+    const bool single = a.cu_q == nullptr;  // one chunk described by the scalar fields
+    if (single) {
         if (tid == 0) {
             const int nt = (a.NQ + cta_q - 1) / cta_q;
             const int t = tile_x;
@@ -283,27 +279,26 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
             }
         }
     }
-    if constexpr (!FULL) __syncthreads();
-    const int s = FULL ? 0 : tile_info[0];
+    __syncthreads();
+    const int s = tile_info[0];
     if (s < 0) return;  // the whole CTA leaves together, before any TMEM or barrier work
-    const int i0 = FULL ? job.i0 : tile_info[1];
+    const int i0 = tile_info[1];
 
     // this chunk's geometry
-    const int q_base = FULL ? job.q_base : single ? 0 : a.cu_q[s];
-    const int NQ = FULL ? job.NQ : single ? a.NQ : a.cu_q[s + 1] - q_base;
-    const int q_start = FULL ? 0 : single ? a.q_start : a.q_starts[s];
-    const int kv_len = FULL ? job.kv_len : single ? a.kv_len : a.kv_lens[s];
-    const int32_t* table = FULL ? job.table : single ? a.block_table : a.block_table + static_cast<size_t>(s) * a.MB;
+    const int q_base = single ? 0 : a.cu_q[s];
+    const int NQ = single ? a.NQ : a.cu_q[s + 1] - q_base;
+    const int q_start = single ? a.q_start : a.q_starts[s];
+    const int kv_len = single ? a.kv_len : a.kv_lens[s];
+    const int32_t* table = single ? a.block_table : a.block_table + static_cast<size_t>(s) * a.MB;
     const int n_table = (kv_len + a.S - 1) / a.S;
-    if (!FULL && (kv_len < q_start + NQ || q_start < 0 || n_table > (single ? a.n_table : a.MB))) {
+    if (kv_len < q_start + NQ || q_start < 0 || n_table > (single ? a.n_table : a.MB)) {
         if (tid == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
         return;
     }
     const bool has_b = i0 + rows_q < NQ;  // query tile B holds at least one token of the chunk
     const int last_q = min(i0 + cta_q, NQ) - 1;
     const int max_key = min(kv_len - 1, q_start + last_q);
-    const int n_tiles = FULL ? job.n_tiles : max_key / kKeys + 1;
-    const int j_base = FULL ? job.j0 : 0;  // the first key tile
+    const int n_tiles = max_key / kKeys + 1;
     const int blocks_per_tile = kKeys / a.S;
     // One-byte caches: with both query tiles live the tensor pipe has work enough to hide the widening and the
     // producer widens every row, leaving the MMA warps to issue; in a varlen launch a CTA with tile A alone (a
@@ -381,11 +376,10 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
         const int full = is_v ? kBarVFull : kBarKFull, empty = is_v ? kBarVEmpty : kBarKEmpty;
         const uint32_t dst0 = sb + (is_v ? kOffV : kOffK);
         auto entry = [&](int idx) { return idx < n_table ? __ldg(table + idx) : -1; };
-        int cur_c = FULL ? (j_base * blocks_per_tile) >> 5 : 0;
-        int cur = entry(cur_c * 32 + lane), nxt = entry(cur_c * 32 + 32 + lane);
+        int cur_c = 0, cur = entry(lane), nxt = entry(32 + lane);
         // this lane's pool row for block `lane` of key tile jj (tiles asked for in increasing order)
         auto tile_row = [&](int jj) {
-            const int idx0 = (j_base + jj) * blocks_per_tile;  // blocks_per_tile divides 32: a tile stays in one batch
+            const int idx0 = jj * blocks_per_tile;  // blocks_per_tile divides 32: a tile stays in one batch
             if ((idx0 >> 5) != cur_c) {
                 cur = nxt;
                 cur_c = idx0 >> 5;
@@ -638,7 +632,7 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
                     w1[k] = chunk(1, k);
                     amax_bits = amax4(amax4(amax_bits, w1[k]), chunk(0, k));
                 }
-                if (amax_bits >= 0x7f800000u && (!FULL || qi < NQ)) raise_error(a.err, PKV_DEVERR_Q_RANGE);  // inf or NaN
+                if (amax_bits >= 0x7f800000u) raise_error(a.err, PKV_DEVERR_Q_RANGE);  // inf or NaN
                 const int ex = static_cast<int>(amax_bits >> 23) - 127;        // floor(log2(max |x|))
                 const int e = min(126, max(-126, 7 - ex));
                 const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -684,9 +678,7 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = bf16x2_to_float2(ws[k]);
-                        // FULL: rows past the chunk are not its own (16-byte chunk i is in row (i / 8) % 128)
-                        in_range = in_range && ((fabsf(f.x) < 65520.f && fabsf(f.y) < 65520.f) ||
-                                                (FULL && qt0 + ((i >> 3) & (kRows - 1)) / a.G >= NQ));
+                        in_range = in_range && fabsf(f.x) < 65520.f && fabsf(f.y) < 65520.f;
                         ws[k] = f16x2_rn(f.x, f.y);
                     }
                     *reinterpret_cast<uint4*>(qt + i * 16) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
@@ -698,7 +690,7 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
             if (lane == 0) mbar_arrive(bar + 8 * kBarQConv);
         }
         for (int j = 0; active && j < n_tiles; ++j) {
-            const int tile0 = (j_base + j) * kKeys, b = j & 1;
+            const int tile0 = j * kKeys, b = j & 1;
             const uint32_t tS = tmem + kColS + 128 * t + 64 * b + trow;
             if (!__all_sync(kFull, s_ready) &&
                 !__all_sync(kFull, mbar_spin_bounded(bar + 8 * (kBarSFull + 2 * t + b), (j >> 1) & 1,
@@ -711,8 +703,8 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
             tmem_ld64(tS, v);
             // test the next tile's scores now; the answer is used only when that tile starts
             s_ready = j + 1 < n_tiles && mbar_test(bar + 8 * (kBarSFull + 2 * t + (b ^ 1)), ((j + 1) >> 1) & 1);
-            const bool masked = (!FULL && tile0 + kKeys - 1 > q_start + qt0) || (tile0 + kKeys > kv_len);
-            const int lim = (FULL ? kv_len : min(kv_len, qpos + 1)) - tile0;
+            const bool masked = (tile0 + kKeys - 1 > q_start + qt0) || (tile0 + kKeys > kv_len);
+            const int lim = min(kv_len, qpos + 1) - tile0;
             float mx[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
@@ -816,35 +808,14 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
         tc_fence_after();
         if (active) {
             const bool store = ok && qi < NQ;
-            if constexpr (FULL) {
-                if (job.rec_o != nullptr) {  // unnormalised O, the running maximum (log2 units) and sum
-                    const size_t row = job.rec_by_token
-                                           ? static_cast<size_t>(q_base + qi) * a.Hq + static_cast<size_t>(h) * a.G + r % a.G
-                                           : static_cast<size_t>(t * kRows + r);
-                    float4* rrow = reinterpret_cast<float4*>(job.rec_o + row * 128);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float o[64];
-                        tmem_ld64(tO + 64 * c, o);
-                        if (store) {
-#pragma unroll
-                            for (int q4 = 0; q4 < 16; ++q4)
-                                rrow[16 * c + q4] = make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-                        }
-                    }
-                    if (store) job.rec_ml[row] = make_float2(m_ref, l_run);
-                }
-            }
-            const bool store_out = store && (!FULL || job.rec_o == nullptr);
             const float inv = l_run > 0.f ? out_mul / l_run : 0.f;
             uint8_t* orow = reinterpret_cast<uint8_t*>(a.out) +
                             (static_cast<size_t>(q_base + qi) * a.Hq + static_cast<size_t>(h) * a.G + r % a.G) * 256;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (FULL && job.rec_o != nullptr) break;
                 float o[64];
                 tmem_ld64(tO + 64 * c, o);  // warp-collective: every lane loads, valid rows store
-                if (store_out) {
+                if (store) {
 #pragma unroll
                     for (int q4 = 0; q4 < 8; ++q4) {
                         uint4 w;
