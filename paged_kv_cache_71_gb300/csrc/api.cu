@@ -1159,9 +1159,9 @@ static pkv_status full_setup(PrefillArgs* out_a, CUtensorMap* qm, CUtensorMap* k
     const int Hkv = c.num_kv_heads, S = c.block_size, G = Hq / Hkv;
     const bool nar = narrow(c.dtype);
     const float kLog2e = 1.4426950408889634f;
-    // key tiles of the whole stream, at most: the kernel counts them in 32 bits
-    const int64_t kt = (static_cast<int64_t>(MB) * S + 63) / 64;
-    if ((static_cast<int64_t>(tokens) / (2 * (128 / G)) + chunks) * Hkv * kt > INT32_MAX - 4096)
+    // units of the whole stream, at most: the kernel counts them in 32 bits
+    const int64_t units = 2 * ((static_cast<int64_t>(MB) * S + 63) / 64) + 32;
+    if ((static_cast<int64_t>(tokens) / (2 * (128 / G)) + chunks) * Hkv * units > INT32_MAX - 4096)
         return fail(PKV_ERR_OUT_OF_RANGE, "query tiles * num_kv_heads * key tiles must stay below 2^31");
     PrefillArgs a;
     a.out = out;
@@ -1458,7 +1458,7 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention launch");
-    e = launch_full_combine(pa, fa, di.sms, s);
+    e = launch_join_cuts(pa, fa, di.sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention join launch");
     return PKV_OK;
 }

@@ -153,8 +153,8 @@ struct PrefixArgs {
     const float* rec_o;          // [rows][128]
     const float2* rec_ml;        // [rows] (m in log2 units, l)
     int64_t extra_row;           // the first row of the CTAs' own pieces
-    const int4* seq_plan;        // [B] {stream position of KV head 0's item, key tiles per item, row in the tile, -}
-    const int* share;            // key tiles per CTA of the prefix kernel
+    const int4* seq_plan;        // [B] {first key tile's unit of KV head 0's item, units per item, row in it, its tiles' units}
+    const int* share;            // stream units per CTA of the prefix kernel
 };
 
 // Until the prefix kernel has completed, its results visible (the decode is launched while it runs).
@@ -169,7 +169,7 @@ __device__ __forceinline__ PrefixPieces prefix_pieces(const PrefixArgs& px, int 
     const int4 sp = __ldcg(px.seq_plan + s);
     const int share = __ldcg(px.share);
     const int U0 = sp.x + h * sp.y, c0 = U0 / share;
-    return {c0, (U0 + sp.y - 1) / share - c0, sp.z};
+    return {c0, (U0 + sp.w - 1) / share - c0, sp.z};
 }
 // Row of piece k of the (s, query head hq) row, gi being hq's place in its group.
 __device__ __forceinline__ size_t prefix_row(const PrefixArgs& px, const PrefixPieces& pp, int k, int s, int Hq, int hq,

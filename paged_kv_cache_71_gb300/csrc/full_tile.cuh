@@ -1,4 +1,4 @@
-// full_tile.cuh -- arguments and launchers of the unmasked attention tile (full_tile.cu): cross attention, and the
+// full_tile.cuh -- arguments and launchers of the unmasked attention stream (full_tile.cu): cross attention, and the
 // shared prefixes of a decode batch.
 #pragma once
 
@@ -6,25 +6,28 @@
 
 namespace pkv {
 
-// Partial records: base rows (one per query token and query head: an item's first piece), then 256 rows for every CTA
-// (the piece with which a CTA's share starts inside an item).
+// Chunks, each a run of query tokens and the keys they all attend to:
+//   cross attention: sequence s, query tokens [cu_q[s], cu_q[s + 1]), keys [0, kv_lens[s]) of table row s;
+//   shared prefixes: group g, tokens = sequences [cu_q[g], cu_q[g + 1]), keys [0, kv_lens[g]) of its first sequence's row.
+// An item is one or two query tiles (128 rows each: token x query head of the group) of one KV head of a chunk.
 struct FullArgs {
-    float* rec_o;        // [rows][128] unnormalised O
-    float2* rec_ml;      // [rows] (running maximum in log2 units, sum)
-    int64_t extra_row;   // first row of the CTAs' own pieces: total_q_tokens * Hq
-    int4* cuts;          // [CTAs] the item that CTA c's share starts inside of (CutItem)
-    int4* seq_plan;      // prefix form: [num_seqs] (SeqPlan), else nullptr
-    int* share;          // key tiles per CTA
-    bool prefix;         // chunks are groups: chunk g's table row is that of its first token (sequence)
+    // partial records (O unnormalised, m in log2 units, l): one row per (token, query head) for an item's first piece, then
+    // 256 rows for every CTA, for the piece with which its share starts inside an item
+    float* rec_o;        // [rows][128]
+    float2* rec_ml;      // [rows]
+    int64_t extra_row;   // first row of the CTAs': total_q_tokens * Hq
+    int* share;          // stream units per CTA
+    int4* cuts;          // [CTAs] {first token, tokens | head << 16, U0, U1} of the item that the CTA's share starts inside
+                         // of, at units [U0, U1) of the stream; U1 = 0: none
+    int4* seq_plan;      // shared prefixes: [sequences] {first key tile's unit of KV head 0's item, units per item, row in the
+                         // item, units of its key tiles}
+    bool prefix;         // shared prefixes: every item leaves records
 };
-
-// cuts[c] = {first query token's row of q, valid rows | h << 16, U0, U1}: CTA c's share starts strictly inside the item
-// whose key tiles are stream positions [U0, U1); U1 = 0: it does not.
-// seq_plan[s] = {U0 of the tile's head 0, key tiles per item, row of the sequence's first query head in its tile, 0}.
 
 size_t paged_full_smem_bytes(int narrow);
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const PrefillArgs& a, const FullArgs& f, int narrow, int grid, cudaStream_t stream);
-cudaError_t launch_full_combine(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream);
+// Joins the pieces of the cut items (cross attention).
+cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream);
 
 }  // namespace pkv

@@ -151,6 +151,11 @@ def test_per_head_scales(kv):
     _check(Batch(RAGGED, 2, 4, 16, kv, seed=5, head_scales=True), f"{kv} per-head scales")
 
 
+def test_more_items_than_a_block_lists_at_a_time():
+    """160 groups of 128 KV heads: 20480 prefixes of one key tile, so that a share has more items than are listed at once."""
+    _check(Batch([(16, [1, i % 3]) for i in range(160)], 128, 1, 16, "bf16", seed=16), "many items", range(0, 320, 23))
+
+
 def test_single_sequence_and_no_prefix_at_all():
     _check(Batch([(0, [1])], 8, 4, 16, "bf16", seed=6), "one token")
     _check(Batch([(16, [0])], 8, 4, 16, "bf16", seed=6), "one block, no own tokens")
