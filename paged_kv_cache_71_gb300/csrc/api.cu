@@ -1103,34 +1103,43 @@ PKV_API pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t ma
 
 // ------------------------------------------------------------------ attention without a mask: shared prefixes, cross
 
-// Scratch of the unmasked tile (full_tile.cu): the cut items and the share, the sequences' plan (shared prefixes), then
-// the partial records' (m, l) and O, one row per (query token, query head) and 256 per CTA.
+// Scratch of the unmasked stream (full_tile.cu): the share, the cut items, with prefixes the sequences' plan and prefix
+// blocks, then the partial records' (m, l) and O: one row per (query token, query head), with prefixes a second one for the
+// sequences' own blocks, and 256 per CTA.
 struct FullScratch {
-    size_t cuts, share, plan, ml, o, total;  // byte offsets, and the whole
+    size_t share, cuts, plan, blocks, ml, o, total;  // byte offsets, and the whole
+    size_t own_row, extra_row;
 };
-static FullScratch full_scratch(int sms, int tokens, int Hq, int plan_seqs) {
+static FullScratch full_scratch(int sms, int tokens, int Hq, bool prefix) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t rows = static_cast<size_t>(tokens) * Hq + static_cast<size_t>(sms) * 256;
     FullScratch f;
-    f.cuts = 0;
-    f.share = up(static_cast<size_t>(sms) * 16);
-    f.plan = f.share + 256;
-    f.ml = f.plan + up(static_cast<size_t>(plan_seqs) * 16);
+    f.own_row = static_cast<size_t>(tokens) * Hq;
+    f.extra_row = f.own_row * (prefix ? 2 : 1);
+    const size_t rows = f.extra_row + static_cast<size_t>(sms) * 256;
+    f.share = 0;
+    f.cuts = 256;
+    f.plan = f.cuts + up(static_cast<size_t>(sms) * 16);
+    f.blocks = f.plan + (prefix ? up(static_cast<size_t>(tokens) * 16) : 0);
+    f.ml = f.blocks + (prefix ? up(static_cast<size_t>(tokens) * 4) : 0);
     f.o = f.ml + up(rows * 8);
     f.total = f.o + rows * 512 + 256;  // the caller's base may be aligned to 16 bytes only
     return f;
 }
 
-static FullArgs full_args(const FullScratch& f, void* base, int tokens, int Hq, bool prefix) {
+static FullArgs full_args(const FullScratch& f, void* base, const int32_t* lens, int num_seqs) {
     uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
     FullArgs a;
     a.rec_o = reinterpret_cast<float*>(p + f.o);
     a.rec_ml = reinterpret_cast<float2*>(p + f.ml);
-    a.extra_row = static_cast<int64_t>(tokens) * Hq;
-    a.cuts = reinterpret_cast<int4*>(p + f.cuts);
-    a.seq_plan = prefix ? reinterpret_cast<int4*>(p + f.plan) : nullptr;
+    a.own_row = static_cast<int64_t>(f.own_row);
+    a.extra_row = static_cast<int64_t>(f.extra_row);
     a.share = reinterpret_cast<int*>(p + f.share);
-    a.prefix = prefix;
+    a.cuts = reinterpret_cast<int4*>(p + f.cuts);
+    a.seq_plan = num_seqs ? reinterpret_cast<int4*>(p + f.plan) : nullptr;
+    a.prefix_blocks = reinterpret_cast<int*>(p + f.blocks);
+    a.lens = lens;
+    a.num_seqs = num_seqs;
+    a.prefix = num_seqs > 0;
     return a;
 }
 
@@ -1204,7 +1213,7 @@ static int prefix_heads_per_unit(int G, int Hkv, int dtype) {
 
 // Scratch of the shared-prefix decode: the unmasked tile's, then the decode's counters and records.
 static size_t prefix_decode_offset(int sms, int B, int Hq) {
-    return (full_scratch(sms, B, Hq, B).total + 255) / 256 * 256;
+    return (full_scratch(sms, B, Hq, true).total + 255) / 256 * 256;
 }
 static size_t prefix_workspace_bytes(int sms, int B, int Hq, int Hkv, int dtype) {
     const int G = Hq / Hkv;
@@ -1308,8 +1317,7 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
     if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, num_seqs, num_q_heads, cu_groups,
                          prefix_lens, num_groups, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
         return st;
-    const FullArgs fa = full_args(full_scratch(di.sms, num_seqs, num_q_heads, num_seqs), workspace, num_seqs,
-                                  num_q_heads, true);
+    const FullArgs fa = full_args(full_scratch(di.sms, num_seqs, num_q_heads, true), workspace, context_lens, num_seqs);
 
     // ---- the sequences' own blocks
     const float kLog2e = 1.4426950408889634f;
@@ -1364,11 +1372,9 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
     px.cu_groups = cu_groups;
     px.prefix_lens = prefix_lens;
     px.num_groups = num_groups;
-    px.rec_o = fa.rec_o;
-    px.rec_ml = fa.rec_ml;
-    px.extra_row = fa.extra_row;
-    px.seq_plan = fa.seq_plan;
-    px.share = fa.share;
+    px.rec_o = fa.rec_o + fa.own_row * 128;
+    px.rec_ml = fa.rec_ml + fa.own_row;
+    px.prefix_blocks = const_cast<int*>(fa.prefix_blocks);
 
     // the counters are cleared first: the decode follows the prefix kernel directly, so that it may start beside it
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1380,6 +1386,8 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
         : nk == 1 ? dispatch_prefix<KvE4M3>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s)
                   : dispatch_prefix<KvI8>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s);
     if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode launch");
+    e = launch_join_rows(pa, fa, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix join launch");
     return PKV_OK;
 }
 
@@ -1396,7 +1404,7 @@ PKV_API pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;
     const int G = num_q_heads / Hkv;
-    size_t need = full_scratch(di.sms, total_q_tokens, num_q_heads, 0).total;
+    size_t need = full_scratch(di.sms, total_q_tokens, num_q_heads, false).total;
     if (total_q_tokens == num_seqs && (G == 1 || G == 2 || G == 4 || G == 8))  // may come as single tokens
         need = std::max(need, workspace_bytes_for(di.sms, num_seqs, Hkv, G, cache->head_dim, cache->dtype));
     *bytes = need;
@@ -1441,7 +1449,7 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
         return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;
-    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, 0);
+    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, false);
     if (!workspace || workspace_bytes < fs.total)
         return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", fs.total,
                     workspace ? workspace_bytes : static_cast<size_t>(0));
@@ -1454,7 +1462,7 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
     if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
                          num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
         return st;
-    const FullArgs fa = full_args(fs, workspace, total_q_tokens, num_q_heads, false);
+    const FullArgs fa = full_args(fs, workspace, nullptr, 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention launch");

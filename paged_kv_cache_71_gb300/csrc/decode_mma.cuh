@@ -143,40 +143,16 @@ __device__ __forceinline__ void threads_sync(int nthreads) {
 constexpr int kCostUnit = 16;  // the weighted split's CTA costs are in 1/16 stream items
 
 // A batch whose sequences share prefixes (pkv_paged_attention_decode_prefix): the decode streams every sequence's own
-// blocks only and joins its (O, m, l) with the prefix's, which full_tile.cu computed for the whole group and left as
-// records: one row per (sequence, query head) for an item's first piece, 256 rows per CTA of that kernel for the piece
-// its share starts with.
+// blocks only.  A sequence with a prefix gets a record (O, m, l) of them, one row per query head, which join_rows_kernel
+// (full_tile.cu) joins with the prefix's; one without gets its output row here.
 struct PrefixArgs {
     const int32_t* cu_groups;    // [num_groups + 1]
     const int32_t* prefix_lens;  // [num_groups], multiples of S
     int num_groups;
-    const float* rec_o;          // [rows][128]
-    const float2* rec_ml;        // [rows] (m in log2 units, l)
-    int64_t extra_row;           // the first row of the CTAs' own pieces
-    const int4* seq_plan;        // [B] {first key tile's unit of KV head 0's item, units per item, row in it, its tiles' units}
-    const int* share;            // stream units per CTA of the prefix kernel
+    float* rec_o;                // [B * Hq][128] unnormalised O
+    float2* rec_ml;              // [B * Hq] (m in log2 units, l)
+    int* prefix_blocks;          // [B] blocks of the sequence's prefix, -1: bad lengths, the row is zero
 };
-
-// Until the prefix kernel has completed, its results visible (the decode is launched while it runs).
-__device__ __forceinline__ void wait_prefix_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// The records of (sequence s, KV head h): piece 0 in the rows of (s, query head), pieces 1 .. n in the rows of CTAs
-// c0 + 1 .. c0 + n, at row_in of their 256.
-struct PrefixPieces {
-    int c0, n, row_in;
-};
-__device__ __forceinline__ PrefixPieces prefix_pieces(const PrefixArgs& px, int s, int h) {
-    const int4 sp = __ldcg(px.seq_plan + s);
-    const int share = __ldcg(px.share);
-    const int U0 = sp.x + h * sp.y, c0 = U0 / share;
-    return {c0, (U0 + sp.w - 1) / share - c0, sp.z};
-}
-// Row of piece k of the (s, query head hq) row, gi being hq's place in its group.
-__device__ __forceinline__ size_t prefix_row(const PrefixArgs& px, const PrefixPieces& pp, int k, int s, int Hq, int hq,
-                                             int gi) {
-    return k == 0 ? static_cast<size_t>(s) * Hq + hq
-                  : static_cast<size_t>(px.extra_row) + static_cast<size_t>(pp.c0 + k) * 256 + pp.row_in + gi;
-}
 
 // PREFIX: the streams hold the sequences' own blocks, off[s] blocks into their tables (-1: a sequence whose length or
 // group is bad; its row is zero); off is in shared memory behind the prefix sums.
@@ -233,6 +209,7 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
                 bad = bad || g0 < 0 || g0 > s || g1 <= s || g1 > B || p < 0 || p % S != 0 || p > L;
                 skip = bad ? 0 : p / S;
                 P[B + 1 + s] = bad ? -1 : skip;
+                if (s % ncta == cta) px.prefix_blocks[s] = P[B + 1 + s];
             }
             if (bad) {
                 if (cta == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
@@ -277,7 +254,7 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
     // ---- 2. empty sequences get zero rows (spread over the CTAs)
     for (int s = cta; s < B; s += ncta) {
         if (P[s + 1] != P[s]) continue;
-        if (PREFIX && off[s] > 0) continue;  // the prefix alone: the kernel's last step
+        if (PREFIX && off[s] > 0) continue;  // the prefix alone
         const int n = a.Hq * D;
         for (int i = tid; i < n; i += nthreads) reinterpret_cast<uint16_t*>(a.out)[static_cast<size_t>(s) * n + i] = 0;
     }
@@ -592,16 +569,13 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
         const int hh = r_row / G;
         if constexpr (PREFIX) {
             if (off[s] > 0) {
-                wait_prefix_kernel();
-                const PrefixPieces pp = prefix_pieces(px, s, u * HP + hh);
-                for (int k = 0; k <= pp.n; ++k) {
-                    const size_t row = prefix_row(px, pp, k, s, a.Hq, u * GU + r_row, r_row % G);
-                    const float2 ml = __ldcg(px.rec_ml + row);
-                    float4 ov[NV];
+                const size_t row = static_cast<size_t>(s) * a.Hq + static_cast<size_t>(u) * GU + r_row;
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) ov[i] = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * D + d0) + i);
-                    combine(ml.x, ml.y, ov);
-                }
+                for (int i = 0; i < NV; ++i)
+                    reinterpret_cast<float4*>(px.rec_o + row * D + d0)[i] =
+                        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                if (lane % LPR == 0) px.rec_ml[row] = make_float2(Mx, Ls);
+                return;
             }
         }
         const float inv = Ls > 0.f ? out_mul(u, hh) / Ls : 0.f;
@@ -905,32 +879,18 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
                 for (int hh = 0; hh < HP; ++hh) {
                     float v[32];
                     o_row(o, hh, v);
-                    float l = l_run[hh];
                     if constexpr (PREFIX) {
                         if (off[s] > 0) {
-                            wait_prefix_kernel();
-                            const PrefixPieces pp = prefix_pieces(px, s, u * HP + hh);
-                            float m = m_ref[hh];
-                            for (int k = 0; k <= pp.n; ++k) {
-                                const size_t row = prefix_row(px, pp, k, s, a.Hq, (u * HP + hh) * G + g, g);
-                                const float2 ml = __ldcg(px.rec_ml + row);
-                                const float mn = fmaxf(m, ml.x);
-                                const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-                                const float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-                                l = l * w0 + ml.y * w1;
-                                m = mn;
+                            const size_t row = static_cast<size_t>(s) * a.Hq + static_cast<size_t>(u * HP + hh) * G + g;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float4 x = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * D + dim_of(4 * i)));
-                                    v[4 * i] = v[4 * i] * w0 + x.x * w1;
-                                    v[4 * i + 1] = v[4 * i + 1] * w0 + x.y * w1;
-                                    v[4 * i + 2] = v[4 * i + 2] * w0 + x.z * w1;
-                                    v[4 * i + 3] = v[4 * i + 3] * w0 + x.w * w1;
-                                }
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(px.rec_o + row * D + dim_of(4 * i)) =
+                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            if (t == 0) px.rec_ml[row] = make_float2(m_ref[hh], l_run[hh]);
+                            continue;
                         }
                     }
-                    store_row(s, u, hh, v, l > 0.f ? out_mul(u, hh) / l : 0.f);
+                    store_row(s, u, hh, v, l_run[hh] > 0.f ? out_mul(u, hh) / l_run[hh] : 0.f);
                 }
             }
             resolve_pending();
@@ -985,41 +945,18 @@ __global__ void __launch_bounds__(32 * kMmaWarps, 1)
                                          nullptr);
 }
 
-// The decode of sequences that share prefixes (decode_prefix_*.cu), launched while the prefix kernel runs.
+// The decode of the own blocks of sequences that share prefixes (decode_prefix_*.cu), launched while the prefix kernel
+// runs: it reads nothing of what that one writes, and takes over its SMs.
 template <int G, int S, class KV, int HP>
 __global__ void __launch_bounds__(32 * kMmaWarps, 1)
     paged_decode_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                const DecodeArgs a, const PrefixArgs px) {
     extern __shared__ uint8_t smem_raw[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     decode_mma_body<G, S, KV, HP, false, true>(kmap, vmap, a, smem_raw, blockIdx.x, gridDim.x, blockDim.x, nullptr,
                                                nullptr, px);
-    wait_prefix_kernel();  // in every warp: this kernel does not end before the prefix kernel
-    // sequences that are their prefix and nothing more: a warp per sequence, four head dims per lane
-    const int* P = reinterpret_cast<const int*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    for (int s = blockIdx.x * nw + warp; s < a.B; s += gridDim.x * nw) {
-        if (P[s + 1] != P[s] || P[a.B + 1 + s] <= 0) continue;
-        for (int hq = 0; hq < a.Hq; ++hq) {
-            const PrefixPieces pp = prefix_pieces(px, s, hq / G);
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k <= pp.n; ++k) {
-                const size_t row = prefix_row(px, pp, k, s, a.Hq, hq, hq % G);
-                const float2 ml = __ldcg(px.rec_ml + row);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(px.rec_o + row * 128) + lane);
-                const float mn = fmaxf(m, ml.x);
-                const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-                const float w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-                l = l * w0 + ml.y * w1;
-                m = mn;
-                o = make_float4(o.x * w0 + x.x * w1, o.y * w0 + x.y * w1, o.z * w0 + x.z * w1, o.w * w0 + x.w * w1);
-            }
-            const float mul = a.v_head ? __ldg(a.v_head + hq / G) : a.o_mul;
-            const float inv = l > 0.f ? mul / l : 0.f;
-            reinterpret_cast<uint2*>(a.out)[(static_cast<size_t>(s) * a.Hq + hq) * 32 + lane] =
-                make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv));
-        }
-    }
+    // in every warp: this kernel does not end before the prefix kernel, so that who waits for it has waited for both
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int G, int S, class KV, int HP>

@@ -9,7 +9,7 @@
 // shares, one per CTA (SM); a cut in an item's first kItemUnits falls before it.  An item that is cut, and every item of a
 // shared prefix, leaves a partial record for each of its pieces; they join as
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i / l
-// in join_cuts_kernel (cross attention) or at the end of the suffix decode (decode_mma.cuh), both launched beside this one.
+// in a kernel launched beside this one: join_cuts_kernel (cross attention), join_rows_kernel (shared prefixes).
 //
 // A CTA runs its share as one stream: TMEM, barriers and the K/V rings live through all of its items, and the copies of
 // the next item's keys run while the current one ends.  Two groups, A and B (128 softmax threads, one per query row, an
@@ -919,6 +919,26 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const PrefillArgs a, con
     }
 }
 
+// Shared prefixes: one warp per (sequence, query head).
+__global__ void __launch_bounds__(256) join_rows_kernel(const PrefillArgs a, const FullArgs f) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= static_cast<size_t>(f.num_seqs) * a.Hq) return;
+    const int s = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq), h = hq / a.G, blocks = f.prefix_blocks[s];
+    const int4 sp = f.seq_plan[s];
+    const int share = *f.share;
+    if (blocks <= 0) return;  // the row is written
+    const int U0 = sp.x + h * sp.y, c0 = U0 / share, c1 = (U0 + sp.w - 1) / share;
+    const size_t extra = static_cast<size_t>(f.extra_row) + sp.z + hq % a.G;
+    Joined j;
+    j.add(f, row, lane);
+    if (f.lens[s] > blocks * a.S) j.add(f, static_cast<size_t>(f.own_row) + row, lane);
+#pragma unroll 4
+    for (int k = c0 + 1; k <= c1; ++k) j.add(f, extra + static_cast<size_t>(k) * 256, lane);
+    j.store(a, row, h, lane);
+}
+
 template <int NARROW>
 static size_t full_smem() {
     return static_cast<size_t>(FullPlan<NARROW>::kOffMeta) + kFEnd + 1024;
@@ -947,10 +967,11 @@ cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, 
     }
 }
 
-// Launched beside the stream kernel: its blocks wait for it where they start.
-cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream) {
+// Launched beside the kernel before it: its blocks wait for it where they start.
+template <class Kernel>
+static cudaError_t launch_beside(Kernel kern, dim3 grid, const PrefillArgs& a, const FullArgs& f, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 8);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -958,7 +979,16 @@ cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_cuts_kernel, a, f);
+    return cudaLaunchKernelEx(&cfg, kern, a, f);
+}
+
+cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream) {
+    return launch_beside(join_cuts_kernel, dim3(grid, 8), a, f, stream);
+}
+
+cudaError_t launch_join_rows(const PrefillArgs& a, const FullArgs& f, cudaStream_t stream) {
+    const size_t rows = static_cast<size_t>(f.num_seqs) * a.Hq;
+    return launch_beside(join_rows_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), a, f, stream);
 }
 
 }  // namespace pkv

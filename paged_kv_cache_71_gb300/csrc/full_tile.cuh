@@ -21,6 +21,10 @@ struct FullArgs {
                          // of, at units [U0, U1) of the stream; U1 = 0: none
     int4* seq_plan;      // shared prefixes: [sequences] {first key tile's unit of KV head 0's item, units per item, row in the
                          // item, units of its key tiles}
+    const int* prefix_blocks;  // [sequences] as the decode of the own blocks found them: > 0 if the row is to be joined
+    const int32_t* lens;       // [sequences] context lengths
+    int num_seqs;
+    int64_t own_row;           // first row of the own blocks' records
     bool prefix;         // shared prefixes: every item leaves records
 };
 
@@ -29,5 +33,7 @@ cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, 
                               const PrefillArgs& a, const FullArgs& f, int narrow, int grid, cudaStream_t stream);
 // Joins the pieces of the cut items (cross attention).
 cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream);
+// Joins every row of a sequence with a prefix: its pieces, and the record of the sequence's own blocks.
+cudaError_t launch_join_rows(const PrefillArgs& a, const FullArgs& f, cudaStream_t stream);
 
 }  // namespace pkv
