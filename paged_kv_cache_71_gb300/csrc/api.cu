@@ -1104,13 +1104,13 @@ PKV_API pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t ma
 // ------------------------------------------------------------------ attention without a mask: shared prefixes, cross
 
 // Scratch of the unmasked stream (full_tile.cu): the share, the cut items, with prefixes the sequences' plan and prefix
-// blocks, then the partial records' (m, l) and O: one row per (query token, query head), with prefixes a second one for the
+// blocks, for one-byte caches the queries' operands and scales, then the partial records' (m, l) and O: one row per (query token, query head), with prefixes a second one for the
 // sequences' own blocks, and 256 per CTA.
 struct FullScratch {
-    size_t share, cuts, plan, blocks, ml, o, total;  // byte offsets, and the whole
+    size_t share, cuts, plan, blocks, q_ops, q_scale, ml, o, total;  // byte offsets, and the whole
     size_t own_row, extra_row;
 };
-static FullScratch full_scratch(int sms, int tokens, int Hq, bool prefix) {
+static FullScratch full_scratch(int sms, int tokens, int Hq, int dtype, bool prefix) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     FullScratch f;
     f.own_row = static_cast<size_t>(tokens) * Hq;
@@ -1120,15 +1120,21 @@ static FullScratch full_scratch(int sms, int tokens, int Hq, bool prefix) {
     f.cuts = 256;
     f.plan = f.cuts + up(static_cast<size_t>(sms) * 16);
     f.blocks = f.plan + (prefix ? up(static_cast<size_t>(tokens) * 16) : 0);
-    f.ml = f.blocks + (prefix ? up(static_cast<size_t>(tokens) * 4) : 0);
+    f.q_ops = f.blocks + (prefix ? up(static_cast<size_t>(tokens) * 4) : 0);
+    f.q_scale = f.q_ops + (narrow(dtype) ? f.own_row * 256 : 0);
+    f.ml = f.q_scale + (narrow(dtype) ? up(f.own_row * 4) : 0);
     f.o = f.ml + up(rows * 8);
     f.total = f.o + rows * 512 + 256;  // the caller's base may be aligned to 16 bytes only
     return f;
 }
 
+static uint8_t* full_base(void* base) {
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
+}
 static FullArgs full_args(const FullScratch& f, void* base, const int32_t* lens, int num_seqs) {
-    uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
+    uint8_t* p = full_base(base);
     FullArgs a;
+    a.q_scale = reinterpret_cast<const float*>(p + f.q_scale);
     a.rec_o = reinterpret_cast<float*>(p + f.o);
     a.rec_ml = reinterpret_cast<float2*>(p + f.ml);
     a.own_row = static_cast<int64_t>(f.own_row);
@@ -1212,14 +1218,14 @@ static int prefix_heads_per_unit(int G, int Hkv, int dtype) {
 }
 
 // Scratch of the shared-prefix decode: the unmasked tile's, then the decode's counters and records.
-static size_t prefix_decode_offset(int sms, int B, int Hq) {
-    return (full_scratch(sms, B, Hq, true).total + 255) / 256 * 256;
+static size_t prefix_decode_offset(int sms, int B, int Hq, int dtype) {
+    return (full_scratch(sms, B, Hq, dtype, true).total + 255) / 256 * 256;
 }
 static size_t prefix_workspace_bytes(int sms, int B, int Hq, int Hkv, int dtype) {
     const int G = Hq / Hkv;
     const size_t tickets = ((static_cast<size_t>(B) * Hkv * 4 + 255) / 256) * 256;
     const size_t rows = static_cast<size_t>(G) * prefix_heads_per_unit(G, Hkv, dtype);
-    return prefix_decode_offset(sms, B, Hq) + tickets + static_cast<size_t>(sms) * kMmaWarps * 2 * rows * (128 + 2) * 4;
+    return prefix_decode_offset(sms, B, Hq, dtype) + tickets + static_cast<size_t>(sms) * kMmaWarps * 2 * rows * (128 + 2) * 4;
 }
 
 PKV_API pkv_status pkv_paged_attention_decode_prefix_workspace_size(const pkv_cache_desc* cache, int32_t num_seqs,
@@ -1312,17 +1318,19 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
         return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the prefix tile");
 
     // ---- the prefixes, each for its whole group
+    const FullScratch fs = full_scratch(di.sms, num_seqs, num_q_heads, cache->dtype, true);
+    const FullArgs fa = full_args(fs, workspace, context_lens, num_seqs);
+    uint8_t* q_ops = full_base(workspace) + fs.q_ops;
     PrefillArgs pa;
     CUtensorMap qm, km, vm;
-    if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, num_seqs, num_q_heads, cu_groups,
+    if ((st = full_setup(&pa, &qm, &km, &vm, out, nk ? q_ops : q, k_cache, v_cache, *cache, num_seqs, num_q_heads, cu_groups,
                          prefix_lens, num_groups, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
         return st;
-    const FullArgs fa = full_args(full_scratch(di.sms, num_seqs, num_q_heads, true), workspace, context_lens, num_seqs);
 
     // ---- the sequences' own blocks
     const float kLog2e = 1.4426950408889634f;
     const int HP = prefix_heads_per_unit(G, Hkv, cache->dtype);
-    uint8_t* dws = static_cast<uint8_t*>(workspace) + prefix_decode_offset(di.sms, num_seqs, num_q_heads);
+    uint8_t* dws = static_cast<uint8_t*>(workspace) + prefix_decode_offset(di.sms, num_seqs, num_q_heads, cache->dtype);
     DecodeArgs da;
     da.out = out;
     da.q = q;
@@ -1376,11 +1384,12 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
     px.rec_ml = fa.rec_ml + fa.own_row;
     px.prefix_blocks = const_cast<int*>(fa.prefix_blocks);
 
-    // the counters are cleared first: the decode follows the prefix kernel directly, so that it may start beside it
+    // every kernel but the first is launched beside the one before it
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(da.tickets, 0, static_cast<size_t>(num_seqs) * Hkv * 4, s);
-    if (e != cudaSuccess) return cuda_fail(e, "clearing split-KV counters");
-    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
+    cudaError_t e = launch_full_prepare(q, q_ops, const_cast<float*>(fa.q_scale), static_cast<int64_t>(num_seqs) * num_q_heads,
+                                        da.tickets, static_cast<int64_t>(num_seqs) * Hkv, nk, di.sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix preparation launch");
+    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, true, s);
     if (e != cudaSuccess) return cuda_fail(e, "shared-prefix launch");
     e = nk == 0   ? dispatch_prefix<KvBF16>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s)
         : nk == 1 ? dispatch_prefix<KvE4M3>(S, G, HP, kd, vd, da, px, di.sms, nw * 32, smem, s)
@@ -1404,7 +1413,7 @@ PKV_API pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;
     const int G = num_q_heads / Hkv;
-    size_t need = full_scratch(di.sms, total_q_tokens, num_q_heads, false).total;
+    size_t need = full_scratch(di.sms, total_q_tokens, num_q_heads, cache->dtype, false).total;
     if (total_q_tokens == num_seqs && (G == 1 || G == 2 || G == 4 || G == 8))  // may come as single tokens
         need = std::max(need, workspace_bytes_for(di.sms, num_seqs, Hkv, G, cache->head_dim, cache->dtype));
     *bytes = need;
@@ -1449,7 +1458,7 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
         return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;
-    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, false);
+    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, cache->dtype, false);
     if (!workspace || workspace_bytes < fs.total)
         return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", fs.total,
                     workspace ? workspace_bytes : static_cast<size_t>(0));
@@ -1457,14 +1466,21 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
     const int nk = narrow_kind(cache->dtype);
     if (static_cast<size_t>(di.smem_optin) < paged_full_smem_bytes(nk))
         return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the cross-attention tile");
+    uint8_t* q_ops = full_base(workspace) + fs.q_ops;
     PrefillArgs pa;
     CUtensorMap qm, km, vm;
-    if ((st = full_setup(&pa, &qm, &km, &vm, out, q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
+    if ((st = full_setup(&pa, &qm, &km, &vm, out, nk ? q_ops : q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
                          num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
         return st;
     const FullArgs fa = full_args(fs, workspace, nullptr, 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, s);
+    cudaError_t e = cudaSuccess;
+    if (nk) {
+        e = launch_full_prepare(q, q_ops, const_cast<float*>(fa.q_scale), static_cast<int64_t>(total_q_tokens) * num_q_heads,
+                                nullptr, 0, nk, di.sms, s);
+        if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention preparation launch");
+    }
+    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, nk != 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention launch");
     e = launch_join_cuts(pa, fa, di.sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention join launch");

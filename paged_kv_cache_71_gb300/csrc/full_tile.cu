@@ -25,6 +25,8 @@
 //   * INT8 caches: warps 12-15 widen the codes to f16, two warps per operand, half of the rows each.
 // Hand-offs are mbarriers; every wait is bounded.  On a timeout a role records the error and does nothing more, the CTA
 // drains its own MMAs and copies (bounded) and frees TMEM.
+#include <algorithm>
+
 #include "full_tile.cuh"
 #include "prefill_tile.cuh"
 
@@ -55,7 +57,7 @@ struct FullPlan {
 // mbarriers
 constexpr int kFKFull = 0, kFKEmpty = 8, kFVFull = 16, kFVEmpty = 24;  // + stage
 constexpr int kFS = 32, kFP = 36, kFPV = 40;        // + 2 * group + buffer: scores written, P written, P V done
-constexpr int kFQ = 44, kFQConv = 46, kFO = 48;     // + group: Q landed, Q converted, O complete
+constexpr int kFQ = 44, kFO = 48;                   // + group: Q landed, O complete
 constexpr int kFMl = 50, kFTaken = 52;              // + owner: the other group's (m, l) are in shared memory; owner has its O
 constexpr int kFZero = 54;                          // V rows past the last key zeroed (items of two query tiles)
 constexpr int kFVThere = 55;                        // + group: V with rows past the last key has landed
@@ -128,15 +130,14 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     float2* ml_out = reinterpret_cast<float2*>(meta + kFMlOut);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, ncta = gridDim.x;
-    const int rows_q = kRows / a.G, cta_q = 2 * rows_q;
+    const int g_shift = 31 - __clz(a.G);  // G divides 128
+    const int rows_q = kRows >> g_shift, cta_q = 2 * rows_q, cta_shift = 8 - g_shift;
     const int n_chunks = a.nseq;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid < kFBars) {
         const int i = tid;
         int count = 1;
         if (i >= kFP && i < kFP + 4) count = 128;
-        if (i >= kFQConv && i < kFQConv + 2) count = 4;
         if (i >= kFMl && i <= kFZero) count = 128;
         if ((i >= kFKEmpty && i < kFVFull) || (i >= kFVEmpty && i < kFS)) count = 2;
         if (i == kFDrain) count = 4;
@@ -159,16 +160,16 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         Chunk k;
         const int q0 = a.cu_q[c], q1 = a.cu_q[c + 1], kv = a.kv_lens[c];
         const bool bad_q = q0 < 0 || q1 < q0 || q1 > a.NQ;
-        const bool bad = bad_q || kv < 0 || kv > a.MB * a.S || (f.prefix && kv % a.S != 0);
+        const bool bad = bad_q || kv < 0 || kv > a.MB * a.S || (f.prefix && (kv & (a.S - 1)) != 0);
         if (bad && report) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
         k.q0 = bad_q ? 0 : q0;
         k.tokens = bad_q ? 0 : q1 - q0;
         k.keys = bad ? -1 : kv;
         k.table = (f.prefix ? k.q0 : c) * a.MB;
         k.w = k.tokens > rows_q ? 2 : 1;
-        k.kt = k.keys > 0 ? ceil_div(k.keys, kKeys) : 0;
+        k.kt = (max(k.keys, 0) + kKeys - 1) / kKeys;
         k.ku = k.kt > 0 ? (k.kt * k.w + kItemUnits + 1) & ~1 : 0;
-        k.items = k.kt > 0 ? ceil_div(k.tokens, cta_q) * a.Hkv : 0;
+        k.items = k.kt > 0 ? ((k.tokens + cta_q - 1) >> cta_shift) * a.Hkv : 0;
         return k;
     };
     int share;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             }
             if (pass == 1) break;
             int incl = sum;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, incl, o);
                 if (lane >= o) incl += y;
@@ -207,13 +208,14 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
-            int T = 0;
-            run = incl - sum;
+            int before = lane < kNT / 32 ? part[lane] : 0;  // of the warps up to lane's
 #pragma unroll 1
-            for (int w = 0; w < kNT / 32; ++w) {
-                if (w < warp) run += part[w];
-                T += part[w];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, before, o);
+                if (lane >= o) before += y;
             }
+            const int T = __shfl_sync(kFull, before, 31), mine_before = __shfl_sync(kFull, before, max(0, warp - 1));
+            run = incl - sum + (warp ? mine_before : 0);
             share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
             x0 = static_cast<int>(min(static_cast<int64_t>(cta) * share, static_cast<int64_t>(T)));
             x1 = static_cast<int>(min(static_cast<int64_t>(x0) + share, static_cast<int64_t>(T)));
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             if (c < n_chunks) k = load_chunk(c, false);
             const int units = k.items * k.ku;
             int iu = units;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, iu, o);
                 if (lane >= o) iu += y;
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             const int k_hi = k.items == 0 || start + kItemUnits >= x1 ? 0 : min(k.items, ceil_div(x1 - start - kItemUnits, k.ku));
             const int cnt = max(0, k_hi - k_lo);
             int ic = cnt;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, ic, o);
                 if (lane >= o) ic += y;
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         const Chunk k = load_chunk(s, false);
         if (f.prefix) {
             for (int i = tid; i < k.tokens; i += kNT)
-                f.seq_plan[k.q0 + i] = make_int4(first_unit[s] + (i / cta_q) * a.Hkv * k.ku + kItemUnits, k.ku, (i % cta_q) * a.G,
+                f.seq_plan[k.q0 + i] = make_int4(first_unit[s] + (i >> cta_shift) * a.Hkv * k.ku + kItemUnits, k.ku, (i & (cta_q - 1)) << g_shift,
                                                   k.ku - kItemUnits);
         } else if (k.keys == 0) {
             uint4* o = reinterpret_cast<uint4*>(a.out) + static_cast<size_t>(k.q0) * a.Hq * 16;
@@ -329,6 +331,9 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         }
     }
 
+    // the preparing kernel has completed; only then may the next one start, which uses what it cleared
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;  // this role has seen no timeout
     auto give_up = [&]() {
         ok = false;
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     const bool pair = items[i].head_pair >> 16;
                     int x = g + first_tile(t, i, pair);  // this group's next tile
                     if (x < end) {
-                        ok = warp_wait(bar + 8 * ((NARROW ? kFQConv : kFQ) + t), q_n & 1, a.timeout_ns);
+                        ok = warp_wait(bar + 8 * (kFQ + t), q_n & 1, a.timeout_ns);
                         ++q_n;
                     }
 #pragma unroll 1
@@ -434,12 +439,11 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         const uint64_t b0 = k0 + ((st * kStage) >> 4);
                         const uint32_t d = tS + 64 * b;
                         if constexpr (NARROW == 1) {
-                            // E4M3: per 64 head dims (a 16 KB half of the slot) hi codes, then lo codes
+                            // E4M3: the query rows' hi codes in the slot's first 16 KB, their lo codes in the second
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                const uint64_t ak = q0 + (((kk >> 1) * kQHalf + (kk & 1) * 32) >> 4);
-                                tc_mma_f8_warp(d, ak, b0 + 2 * kk, kIdescS8, kk > 0);
-                                tc_mma_f8_warp(d, ak + 4, b0 + 2 * kk, kIdescS8, 1u);
+                                tc_mma_f8_warp(d, q0 + 2 * kk, b0 + 2 * kk, kIdescS8, kk > 0);
+                                tc_mma_f8_warp(d, q0 + (kQHalf >> 4) + 2 * kk, b0 + 2 * kk, kIdescS8, 1u);
                             }
                         } else {
 #pragma unroll
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         if (!ok) break;
                         const uint8_t* src = smem + PL::kOffStg + (is_v * PL::kSlots + slot) * kStgSlot + lane * 128;
                         uint8_t* dst = smem + (is_v ? PL::kOffV : PL::kOffK) + st * kStage + lane * 128;
-#pragma unroll 4
+#pragma unroll 8
                         for (int k = 0; k < 16; ++k) {  // 16 codes: head dims 16 (k & 7) .. + 15 of row lane + 32 (k >> 3)
                             const int c16 = k & 7, ro = (k >> 3) * 32 * 128;
                             const uint4 wv = *reinterpret_cast<const uint4*>(src + ro + ((c16 ^ sw) * 16));
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         const int t = warp >> 2, r = tid & 127;
         const uint32_t trow = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint8_t* q_slot = smem + 2 * t * kQHalf;
-        int c = 0, q_sent = 0, q_seen = 0;    // this group's key tiles; Q copies sent, and found
+        int c = 0, q_sent = 0;                // this group's key tiles; Q copies sent
         int o_mine = 0, o_other = 0;          // items of this group, of the other one
         int joins_mine = 0, joins_other = 0;  // items that this group joined, that the other one did
         int zeroed = 0;                       // key tiles whose V rows past the last key it zeroed
@@ -587,95 +591,13 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 tma_load_3d_nohint(smem_u32(q_slot) + hf * kQHalf, &qmap, hf * 64, (it.head_pair & 0xffff) * a.G, row, qb);
             ++q_sent;
         };
-        // This thread's query row of an item, made ready for the MMAs; what its scores are multiplied by (log2 units).
-        auto ready_q = [&](const Item& it) {
-            float sm_log2 = a.k_head ? a.sm_base * __ldg(a.k_head + (it.head_pair & 0xffff)) : a.sm_log2;
-            if constexpr (NARROW == 0) return sm_log2;
-            const int row = ((it.head_pair >> 16) && t ? kRows : 0) + r;
-            const bool valid = row < it.tokens * a.G, live = (row & ~31) < it.tokens * a.G;
-            if (!warp_wait(bar + 8 * (kFQ + t), q_seen++ & 1, a.timeout_ns)) give_up();
-            if (live && ok) {
-                uint8_t* qt = q_slot + r * 128;
-                const int sw = r & 7;
-                if constexpr (NARROW == 1) {
-                    // The row (bf16: dims 0-63 in the slot's first 16 KB, 64-127 in the second) is scaled by 2^e, e chosen
-                    // so that its largest magnitude lies in [128, 256), and split into hi = E4M3(x) and lo = E4M3(x - hi),
-                    // written over it, per 64 dims 64 bytes of hi codes and 64 of lo codes; hi + lo is the scaled value
-                    // exactly for elements within 2^-10 of the row's largest.  The scores are multiplied back by 2^-e.
-                    uint32_t amax_bits = 0;  // |value| bits: ordered like the values
-#pragma unroll 4
-                    for (int k = 0; k < 16; ++k) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(qt + (k >> 3) * kQHalf + ((k & 7) << 4));
-                        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            amax_bits = max(amax_bits, max((ws[u] << 17) >> 1, ((ws[u] >> 16) & 0x7fffu) << 16));
-                    }
-                    if (amax_bits >= 0x7f800000u && valid) raise_error(a.err, PKV_DEVERR_Q_RANGE);  // inf or NaN
-                    const int ex = static_cast<int>(amax_bits >> 23) - 127;  // floor(log2(max |x|))
-                    const int e = min(126, max(-126, 7 - ex));
-                    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-                    sm_log2 *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll 1
-                    for (int hf = 0; hf < 2; ++hf, qt += kQHalf) {
-                        uint4 x[8];  // dims 8 k .. 8 k + 7 of the half, all read before any is written over
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const uint4*>(qt + ((k ^ sw) << 4));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // dims 16 k .. 16 k + 15
-                            const uint32_t ws[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
-                                                    x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-                            uint32_t hw[4], lw[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float2 f01 = bf16x2_to_float2(ws[2 * u]), f23 = bf16x2_to_float2(ws[2 * u + 1]);
-                                const float v0 = f01.x * up, v1 = f01.y * up, v2 = f23.x * up, v3 = f23.y * up;
-                                const uint32_t h01 = f32x2_to_e4m3x2(v0, v1), h23 = f32x2_to_e4m3x2(v2, v3);
-                                const float2 b01 = f16x2_to_float2(e4m3x2_to_f16x2_u(h01));
-                                const float2 b23 = f16x2_to_float2(e4m3x2_to_f16x2_u(h23));
-                                hw[u] = h01 | (h23 << 16);
-                                lw[u] = f32x2_to_e4m3x2(v0 - b01.x, v1 - b01.y) |
-                                        (f32x2_to_e4m3x2(v2 - b23.x, v3 - b23.y) << 16);
-                            }
-                            *reinterpret_cast<uint4*>(qt + ((k ^ sw) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                            *reinterpret_cast<uint4*>(qt + (((k + 4) ^ sw) << 4)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-                        }
-                    }
-                } else {
-                    // f16 MMAs: the row converted in place, exactly for |q| in [2^-14, 65504]
-                    bool in_range = true;
-#pragma unroll 2
-                    for (int k = 0; k < 16; ++k) {
-                        uint4* p = reinterpret_cast<uint4*>(qt + (k >> 3) * kQHalf + ((k & 7) << 4));
-                        const uint4 w = *p;
-                        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float2 x = bf16x2_to_float2(ws[u]);
-                            in_range = in_range && fabsf(x.x) < 65520.f && fabsf(x.y) < 65520.f;
-                            ws[u] = f16x2_rn(x.x, x.y);
-                        }
-                        *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-                    }
-                    if (!in_range && valid) raise_error(a.err, PKV_DEVERR_Q_RANGE);
-                }
-            }
-            fence_proxy_async_smem();  // the S MMAs (async proxy) read what was written
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + 8 * (kFQConv + t));
-            return sm_log2;
-        };
         batches(std::false_type{}, [&](int n) {
             int i = next_item(0, n), nxt = n;
-            float sm_log2 = 0.f, sm_next = 0.f;
             o_other += i;  // the items of the other group alone
-            if (i < n && ok) {
-                if (r == 0) copy_q(items[i]);
-                __syncwarp();
-                sm_log2 = ready_q(items[i]);
-            }
+            if (i < n && ok && r == 0) copy_q(items[i]);
+            __syncwarp();
 #pragma unroll 1
-            for (; i < n && ok; o_other += nxt - i - 1, i = nxt, sm_log2 = sm_next) {
+            for (; i < n && ok; o_other += nxt - i - 1, i = nxt) {
                 const Item& it = items[i];
                 nxt = next_item(i + 1, n);
                 const bool pair = it.head_pair >> 16;
@@ -684,7 +606,17 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 const int row = (pair && t ? kRows : 0) + r;  // of the item's rows
                 const bool valid = row < it.tokens * a.G;
                 const bool live = (row & ~31) < it.tokens * a.G;  // some row of this warp is the item's
+                const int h = it.head_pair & 0xffff;
+                const size_t tok_row = (static_cast<size_t>(it.q_row) + (row >> g_shift)) * a.Hq + (static_cast<size_t>(h) << g_shift) +
+                                       (row & (a.G - 1));
                 float m_ref = -INFINITY, l_run = 0.f;
+                // what the scores are multiplied by (log2 units)
+                float sm_log2 = a.k_head ? a.sm_base * __ldg(a.k_head + h) : a.sm_log2;
+                if (NARROW != 0 && valid) {
+                    const float s = f.q_scale[tok_row];  // negative: values that the operands cannot carry
+                    if (s < 0.f) raise_error(a.err, PKV_DEVERR_Q_RANGE);
+                    sm_log2 *= fabsf(s);
+                }
                 int left = it.keys - (it.j0 + j_first) * kKeys;  // keys from the current tile on
 #pragma unroll 1
                 for (int j = j_first; j < tiles; j += step, left -= step * kKeys, ++c) {
@@ -785,7 +717,6 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     tc_fence_before();
                     mbar_arrive(bar + 8 * (kFP + 2 * t + b));
                 }
-                if (nxt < n && ok) sm_next = ready_q(items[nxt]);  // its scores are computed while this item is written out
                 ++o_mine;
                 if (pair || split) ++o_other;
                 if (split && t == owner) ++joins_mine;
@@ -816,8 +747,6 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     m_ref = m;
                     l_run = l_run * w_mine + ml.y * w_other;
                 }
-                const int h = it.head_pair & 0xffff;
-                const size_t tok_row = (static_cast<size_t>(it.q_row) + row / a.G) * a.Hq + static_cast<size_t>(h) * a.G + row % a.G;
                 const size_t rec_row = it.rec == 2 ? static_cast<size_t>(f.extra_row) + static_cast<size_t>(cta) * 256 + row : tok_row;
                 const bool rec = it.rec != 0;
                 const float inv = rec ? 1.f : l_run > 0.f ? (a.v_head ? __ldg(a.v_head + h) : a.out_mul) / l_run : 0.f;
@@ -861,7 +790,6 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         if (r == 0 && !ok && q_sent > 0) mbar_wait_bounded(bar + 8 * (kFQ + t), (q_sent - 1) & 1, a.timeout_ns);
     }
     if (!ok && lane == 0) *abort_flag = 1;
-
     // ---- drain: nothing of this CTA may still be in flight when TMEM is freed and the CTA exits
     __syncthreads();
     if (warp >= 8 && (warp & 1) && *abort_flag) {
@@ -939,6 +867,49 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const PrefillArgs a, con
     j.store(a, row, h, lane);
 }
 
+// What precedes the stream: the decode's counters cleared (shared prefixes), and for one-byte caches the queries turned
+// into the MMAs' operands, once for all of the items that use them: 256 bytes a row, and what the row's scores are
+// multiplied by -- negative if a value cannot be carried.  One warp per row (token, query head), four head dims per lane.
+//   FP8: the row is scaled by 2^e, e chosen so that its largest magnitude lies in [128, 256), and split into hi = E4M3(x)
+//   and lo = E4M3(x - hi), 128 bytes each; hi + lo is the scaled value exactly for elements within 2^-10 of the row's
+//   largest.  INT8: f16, exactly for |q| in [2^-14, 65504].
+template <int NARROW>
+__global__ void __launch_bounds__(256) full_prepare_kernel(const uint2* __restrict__ q, uint8_t* __restrict__ ops,
+                                                           float* __restrict__ scale, int64_t rows, int* __restrict__ counters,
+                                                           int64_t n_counters) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256, first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    for (int64_t i = first; i < n_counters; i += stride) counters[i] = 0;
+    if constexpr (NARROW != 0) {
+        for (int64_t row = first >> 5; row < rows; row += stride >> 5) {
+            const uint2 w = q[row * 32 + lane];
+            const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+            uint8_t* out = ops + row * 256;
+            if constexpr (NARROW == 1) {
+                uint32_t m = max(max((w.x << 17) >> 1, (w.x & 0x7fff0000u)), max((w.y << 17) >> 1, (w.y & 0x7fff0000u)));
+                m = __reduce_max_sync(kFull, m);  // |value| bits: ordered like the values
+                const int e = min(126, max(-126, 7 - (static_cast<int>(m >> 23) - 127)));
+                const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                const float v0 = a.x * up, v1 = a.y * up, v2 = b.x * up, v3 = b.y * up;
+                const uint32_t h01 = f32x2_to_e4m3x2(v0, v1), h23 = f32x2_to_e4m3x2(v2, v3);
+                const float2 b01 = f16x2_to_float2(e4m3x2_to_f16x2_u(h01)), b23 = f16x2_to_float2(e4m3x2_to_f16x2_u(h23));
+                reinterpret_cast<uint32_t*>(out)[lane] = h01 | (h23 << 16);
+                reinterpret_cast<uint32_t*>(out)[32 + lane] =
+                    f32x2_to_e4m3x2(v0 - b01.x, v1 - b01.y) | (f32x2_to_e4m3x2(v2 - b23.x, v3 - b23.y) << 16);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                if (lane == 0) scale[row] = m >= 0x7f800000u ? -down : down;  // inf or NaN
+            } else {
+                const bool fits = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))) < 65520.f;
+                const bool number = a.x == a.x && a.y == a.y && b.x == b.x && b.y == b.y;
+                reinterpret_cast<uint2*>(out)[lane] = make_uint2(f16x2_rn(a.x, a.y), f16x2_rn(b.x, b.y));
+                const bool good = __all_sync(kFull, fits && number);
+                if (lane == 0) scale[row] = good ? 1.f : -1.f;
+            }
+        }
+    }
+}
+
 template <int NARROW>
 static size_t full_smem() {
     return static_cast<size_t>(FullPlan<NARROW>::kOffMeta) + kFEnd + 1024;
@@ -946,23 +917,45 @@ static size_t full_smem() {
 
 size_t paged_full_smem_bytes(int narrow) { return narrow == 2 ? full_smem<2>() : narrow == 1 ? full_smem<1>() : full_smem<0>(); }
 
+cudaError_t launch_full_prepare(const void* q, void* ops, float* scale, int64_t rows, int* counters, int64_t n_counters,
+                                int narrow, int sms, cudaStream_t stream) {
+    const int64_t work = std::max<int64_t>(narrow ? rows * 32 : 0, n_counters);
+    const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(sms) * 8, (work + 255) / 256));
+    const uint2* src = static_cast<const uint2*>(q);
+    uint8_t* dst = static_cast<uint8_t*>(ops);
+    if (narrow == 1) full_prepare_kernel<1><<<grid, 256, 0, stream>>>(src, dst, scale, rows, counters, n_counters);
+    else if (narrow == 2) full_prepare_kernel<2><<<grid, 256, 0, stream>>>(src, dst, scale, rows, counters, n_counters);
+    else full_prepare_kernel<0><<<grid, 256, 0, stream>>>(src, dst, scale, rows, counters, n_counters);
+    return cudaGetLastError();
+}
+
 template <int NARROW>
 static cudaError_t launch_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                               const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream) {
+                               const PrefillArgs& a, const FullArgs& f, int grid, bool prepared, cudaStream_t stream) {
     const size_t smem = full_smem<NARROW>();
     auto kern = paged_full_kernel<NARROW>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kern<<<grid, FullPlan<NARROW>::kThreads, smem, stream>>>(qmap, kmap, vmap, a, f);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(FullPlan<NARROW>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = prepared ? 1 : 0;  // beside the preparing kernel; not beside what the caller's stream had before
+    return cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, a, f);
 }
 
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                              const PrefillArgs& a, const FullArgs& f, int narrow, int grid, cudaStream_t stream) {
+                              const PrefillArgs& a, const FullArgs& f, int narrow, int grid, bool prepared,
+                              cudaStream_t stream) {
     switch (narrow) {
-        case 0: return launch_full<0>(qmap, kmap, vmap, a, f, grid, stream);
-        case 1: return launch_full<1>(qmap, kmap, vmap, a, f, grid, stream);
-        case 2: return launch_full<2>(qmap, kmap, vmap, a, f, grid, stream);
+        case 0: return launch_full<0>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 1: return launch_full<1>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 2: return launch_full<2>(qmap, kmap, vmap, a, f, grid, prepared, stream);
         default: return cudaErrorInvalidValue;
     }
 }

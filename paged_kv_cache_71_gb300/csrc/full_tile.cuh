@@ -16,6 +16,7 @@ struct FullArgs {
     float* rec_o;        // [rows][128]
     float2* rec_ml;      // [rows]
     int64_t extra_row;   // first row of the CTAs': total_q_tokens * Hq
+    const float* q_scale;  // one-byte caches: [rows] of (token, query head), what the operands' scores are multiplied by
     int* share;          // stream units per CTA
     int4* cuts;          // [CTAs] {first token, tokens | head << 16, U0, U1} of the item that the CTA's share starts inside
                          // of, at units [U0, U1) of the stream; U1 = 0: none
@@ -30,7 +31,11 @@ struct FullArgs {
 
 size_t paged_full_smem_bytes(int narrow);
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                              const PrefillArgs& a, const FullArgs& f, int narrow, int grid, cudaStream_t stream);
+                              const PrefillArgs& a, const FullArgs& f, int narrow, int grid, bool prepared,
+                              cudaStream_t stream);
+// Before the stream: the queries' operands (one-byte caches), counters cleared.
+cudaError_t launch_full_prepare(const void* q, void* ops, float* scale, int64_t rows, int* counters, int64_t n_counters,
+                                int narrow, int sms, cudaStream_t stream);
 // Joins the pieces of the cut items (cross attention).
 cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream);
 // Joins every row of a sequence with a prefix: its pieces, and the record of the sequence's own blocks.
