@@ -123,9 +123,9 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -258,24 +258,28 @@ def pkv_block_hashes(token_ids, cu_tokens, block_size: int, out_offsets, hashes,
            "pkv_block_hashes")
 
 
-def _expect(func: str, names: str, *wanted) -> None:
-    """Refuse tensors that the pointers alone would not tell from good ones.  Each of `wanted` is (tensor, dtypes, shape);
-    layouts must be contiguous, and every tensor on the current CUDA device."""
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    for t, dtypes, shape in wanted:
-        if not (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device >= 0):
-            break
-    else:
-        return
-    for name, (t, dtypes, shape) in zip(names.split(), wanted):  # something is wrong: say what
+def _device() -> int:
+    """The current CUDA device; a number that no tensor's device has, where CUDA has not been used."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _fits(t, dtype, shape, device: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device
+
+
+def _refuse(func: str, device: int, **tensors) -> None:
+    """Say what is wrong with tensors that the pointers alone would not tell from good ones: name=(tensor or None, dtypes,
+    shape).  Layouts must be contiguous, and every tensor on the current CUDA device."""
+    tensors = {name: x for name, x in tensors.items() if x[0] is not None}
+    for name, (t, dtypes, shape) in tensors.items():
         if t.dtype not in dtypes:
             raise PkvError(1, func, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
         if t.shape != shape:
             raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise PkvError(1, func, f"{name} must be contiguous")
-    for name, (t, _, _) in zip(names.split(), wanted):
-        if device < 0 or t.get_device() != device:
+    for name, (t, _, _) in tensors.items():
+        if t.get_device() != device:
             raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
 
 
@@ -288,37 +292,54 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
                          stream=None) -> None:
     """Block tables, lengths and slot map of a step from the request lengths, on the GPU.  seq_lens may be past_lens and
     new_free_count may be free_count (in place); free_blocks has one entry per block of the pool."""
-    L, n = lib(), past_lens.shape[0]
-    seqs = (n,)
-    _expect("pkv_extend_sequences",
-            "block_tables past_lens new_lens free_blocks free_count seq_lens new_free_count slot_mapping q_starts cu_q",
-            (block_tables, _I32, (n, block_tables.shape[-1])), (past_lens, _I32, seqs), (new_lens, _I32, seqs),
-            (free_blocks, _I32, (free_blocks.numel(),)), (free_count, _I32, (1,)), (seq_lens, _I32, seqs),
-            (new_free_count, _I32, (1,)), (slot_mapping, _I64, (slot_mapping.numel(),)),
-            (past_lens if q_starts is None else q_starts, _I32, seqs),
-            (free_count, _I32, (1,)) if cu_q is None else (cu_q, _I32, (n + 1,)))
-    _check(L.pkv_extend_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(new_lens), n,
-                                  int(block_size), _ptr(free_blocks), _ptr(free_count), free_blocks.shape[0],
-                                  _ptr(seq_lens), _ptr(new_free_count), _ptr(slot_mapping), slot_mapping.shape[0],
-                                  _ptr(cu_q), _ptr(q_starts), _ptr(device_error), _stream(stream)),
-           "pkv_extend_sequences")
+    L, (n,), i32 = lib(), past_lens.shape, torch.int32
+    width, nb, cap, dev = block_tables.shape[-1], free_blocks.numel(), slot_mapping.numel(), _device()
+    if not (block_tables.dtype is past_lens.dtype is new_lens.dtype is free_blocks.dtype is free_count.dtype
+            is seq_lens.dtype is new_free_count.dtype is i32 and slot_mapping.dtype is torch.int64
+            and block_tables.shape == (n, width) and new_lens.shape == seq_lens.shape == past_lens.shape
+            and free_count.shape == new_free_count.shape == (1,) and free_blocks.dim() == slot_mapping.dim() == 1
+            and block_tables.is_contiguous() and past_lens.is_contiguous() and new_lens.is_contiguous()
+            and free_blocks.is_contiguous() and seq_lens.is_contiguous() and slot_mapping.is_contiguous()
+            and block_tables.get_device() == past_lens.get_device() == new_lens.get_device() == free_blocks.get_device()
+            == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device()
+            == slot_mapping.get_device() == dev
+            and (cu_q is None or _fits(cu_q, i32, (n + 1,), dev)) and (q_starts is None or _fits(q_starts, i32, (n,), dev))):
+        _refuse("pkv_extend_sequences", dev, block_tables=(block_tables, _I32, (n, width)), past_lens=(past_lens, _I32, (n,)),
+                new_lens=(new_lens, _I32, (n,)), free_blocks=(free_blocks, _I32, (nb,)), free_count=(free_count, _I32, (1,)),
+                seq_lens=(seq_lens, _I32, (n,)), new_free_count=(new_free_count, _I32, (1,)),
+                slot_mapping=(slot_mapping, _I64, (cap,)), cu_q=(cu_q, _I32, (n + 1,)), q_starts=(q_starts, _I32, (n,)))
+    status = L.pkv_extend_sequences(block_tables.data_ptr(), width, past_lens.data_ptr(), new_lens.data_ptr(), n,
+                                    int(block_size), free_blocks.data_ptr(), free_count.data_ptr(), nb, seq_lens.data_ptr(),
+                                    new_free_count.data_ptr(), slot_mapping.data_ptr(), cap, _ptr(cu_q), _ptr(q_starts),
+                                    _ptr(device_error), _stream(stream, dev))
+    if status:
+        _check(status, "pkv_extend_sequences")
 
 
 def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, free_blocks, free_count, seq_lens,
                           new_free_count, keep_blocks=None, device_error=None, stream=None) -> None:
     """Finished sequences hand their blocks back to the free stack, on the GPU (finished: bool or uint8 [num_seqs])."""
-    L, n = lib(), past_lens.shape[0]
-    seqs = (n,)
-    _expect("pkv_release_sequences",
-            "block_tables past_lens finished free_blocks free_count seq_lens new_free_count keep_blocks",
-            (block_tables, _I32, (n, block_tables.shape[-1])), (past_lens, _I32, seqs), (finished, _FLAG, seqs),
-            (free_blocks, _I32, (free_blocks.numel(),)), (free_count, _I32, (1,)), (seq_lens, _I32, seqs),
-            (new_free_count, _I32, (1,)), (past_lens if keep_blocks is None else keep_blocks, _I32, seqs))
-    _check(L.pkv_release_sequences(_ptr(block_tables), block_tables.shape[1], _ptr(past_lens), _ptr(finished),
-                                   _ptr(keep_blocks), n, int(block_size), _ptr(free_blocks), _ptr(free_count),
-                                   free_blocks.shape[0], _ptr(seq_lens), _ptr(new_free_count), _ptr(device_error),
-                                   _stream(stream)),
-           "pkv_release_sequences")
+    L, (n,), i32 = lib(), past_lens.shape, torch.int32
+    width, nb, dev = block_tables.shape[-1], free_blocks.numel(), _device()
+    if not (block_tables.dtype is past_lens.dtype is free_blocks.dtype is free_count.dtype is seq_lens.dtype
+            is new_free_count.dtype is i32 and finished.dtype in _FLAG
+            and block_tables.shape == (n, width) and finished.shape == seq_lens.shape == past_lens.shape
+            and free_count.shape == new_free_count.shape == (1,) and free_blocks.dim() == 1
+            and block_tables.is_contiguous() and past_lens.is_contiguous() and finished.is_contiguous()
+            and free_blocks.is_contiguous() and seq_lens.is_contiguous()
+            and block_tables.get_device() == past_lens.get_device() == finished.get_device() == free_blocks.get_device()
+            == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device() == dev
+            and (keep_blocks is None or _fits(keep_blocks, i32, (n,), dev))):
+        _refuse("pkv_release_sequences", dev, block_tables=(block_tables, _I32, (n, width)),
+                past_lens=(past_lens, _I32, (n,)), finished=(finished, _FLAG, (n,)), free_blocks=(free_blocks, _I32, (nb,)),
+                free_count=(free_count, _I32, (1,)), seq_lens=(seq_lens, _I32, (n,)),
+                new_free_count=(new_free_count, _I32, (1,)), keep_blocks=(keep_blocks, _I32, (n,)))
+    status = L.pkv_release_sequences(block_tables.data_ptr(), width, past_lens.data_ptr(), finished.data_ptr(),
+                                     _ptr(keep_blocks), n, int(block_size), free_blocks.data_ptr(), free_count.data_ptr(), nb,
+                                     seq_lens.data_ptr(), new_free_count.data_ptr(), _ptr(device_error),
+                                     _stream(stream, dev))
+    if status:
+        _check(status, "pkv_release_sequences")
 
 
 def pkv_paged_attention_decode_prefix_workspace_size(cache: CacheDesc, num_seqs: int, num_q_heads: int) -> int:
@@ -334,21 +355,27 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
                                       stream=None) -> None:
     """Decode attention for groups of sequences (cu_groups) that share their first prefix_lens tokens' blocks: a group's
     prefix is computed once for all of its sequences."""
-    L, (n, heads, D) = lib(), q.shape
-    caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
-    groups = prefix_lens.shape[0]
-    _expect("pkv_paged_attention_decode_prefix",
-            "q out k_cache v_cache block_tables context_lens cu_groups prefix_lens",
-            (q, _FLOATS, (n, heads, cache.head_dim)), (out, (q.dtype,), (n, heads, D)), (k_cache, _CACHES, caches),
-            (v_cache, (k_cache.dtype,), caches), (block_tables, _I32, (n, block_tables.shape[-1])),
-            (context_lens, _I32, (n,)), (cu_groups, _I32, (groups + 1,)), (prefix_lens, _I32, (groups,)))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(L.pkv_paged_attention_decode_prefix(_ptr(out), _ptr(q), _dtype(q), _ptr(k_cache), _ptr(v_cache),
-                                               ctypes.byref(cache), _ptr(block_tables), block_tables.shape[1],
-                                               _ptr(context_lens), n, heads, float(scale), _ptr(cu_groups),
-                                               _ptr(prefix_lens), groups, _ptr(workspace), ws_bytes,
-                                               _ptr(device_error), _stream(stream)),
-           "pkv_paged_attention_decode_prefix")
+    L, (n, heads, D), dev = lib(), q.shape, _device()
+    caches, groups, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), prefix_lens.numel(), block_tables.shape[-1]
+    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES
+            and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
+            and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
+            and _fits(block_tables, torch.int32, (n, width), dev) and _fits(context_lens, torch.int32, (n,), dev)
+            and _fits(cu_groups, torch.int32, (groups + 1,), dev) and _fits(prefix_lens, torch.int32, (groups,), dev)):
+        caches = (*caches[:3], cache.head_dim)
+        _refuse("pkv_paged_attention_decode_prefix", dev, q=(q, _FLOATS, (n, heads, cache.head_dim)),
+                out=(out, (q.dtype,), (n, heads, D)), k_cache=(k_cache, _CACHES, caches),
+                v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
+                context_lens=(context_lens, _I32, (n,)), cu_groups=(cu_groups, _I32, (groups + 1,)),
+                prefix_lens=(prefix_lens, _I32, (groups,)))
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = L.pkv_paged_attention_decode_prefix(out.data_ptr(), q.data_ptr(), _DTYPE_CODE[q.dtype], k_cache.data_ptr(),
+                                                 v_cache.data_ptr(), ctypes.byref(cache), block_tables.data_ptr(), width,
+                                                 context_lens.data_ptr(), n, heads, float(scale), cu_groups.data_ptr(),
+                                                 prefix_lens.data_ptr(), groups, ws, ws_bytes, _ptr(device_error),
+                                                 _stream(stream, dev))
+    if status:
+        _check(status, "pkv_paged_attention_decode_prefix")
 
 
 def pkv_paged_cross_attention_workspace_size(cache: CacheDesc, total_q_tokens: int, num_seqs: int,
@@ -364,19 +391,25 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
                               workspace=None, device_error=None, stream=None) -> None:
     """Decoder queries against paged encoder states, without a mask: sequence s owns query tokens
     [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
-    L, (tokens, heads, D), n = lib(), q.shape, kv_lens.shape[0]
-    caches = (cache.num_blocks, cache.block_size, cache.num_kv_heads, cache.head_dim)
-    _expect("pkv_paged_cross_attention", "q out kv_lens k_cache v_cache block_tables cu_q",
-            (q, _FLOATS, (tokens, heads, cache.head_dim)), (out, (q.dtype,), (tokens, heads, D)), (kv_lens, _I32, (n,)),
-            (k_cache, _CACHES, caches), (v_cache, (k_cache.dtype,), caches),
-            (block_tables, _I32, (n, block_tables.shape[-1])),
-            (kv_lens, _I32, (n,)) if cu_q is None else (cu_q, _I32, (n + 1,)))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(L.pkv_paged_cross_attention(_ptr(out), _ptr(q), _dtype(q), tokens, _ptr(cu_q), _ptr(kv_lens),
-                                       _ptr(k_cache), _ptr(v_cache), ctypes.byref(cache), _ptr(block_tables),
-                                       block_tables.shape[1], n, heads, float(scale), _ptr(workspace), ws_bytes,
-                                       _ptr(device_error), _stream(stream)),
-           "pkv_paged_cross_attention")
+    L, (tokens, heads, D), n, dev = lib(), q.shape, kv_lens.numel(), _device()
+    caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
+    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES
+            and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
+            and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
+            and _fits(block_tables, torch.int32, (n, width), dev) and _fits(kv_lens, torch.int32, (n,), dev)
+            and (cu_q is None or _fits(cu_q, torch.int32, (n + 1,), dev))):
+        caches = (*caches[:3], cache.head_dim)
+        _refuse("pkv_paged_cross_attention", dev, q=(q, _FLOATS, (tokens, heads, cache.head_dim)),
+                out=(out, (q.dtype,), (tokens, heads, D)), kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _CACHES, caches),
+                v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
+                cu_q=(cu_q, _I32, (n + 1,)))
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = L.pkv_paged_cross_attention(out.data_ptr(), q.data_ptr(), _DTYPE_CODE[q.dtype], tokens, _ptr(cu_q),
+                                         kv_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(cache),
+                                         block_tables.data_ptr(), width, n, heads, float(scale), ws, ws_bytes,
+                                         _ptr(device_error), _stream(stream, dev))
+    if status:
+        _check(status, "pkv_paged_cross_attention")
 
 
 def pkv_status_string(status: int) -> str:

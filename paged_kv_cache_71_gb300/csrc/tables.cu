@@ -20,47 +20,49 @@ namespace pkv {
 
 namespace {
 
-// Block-wide exclusive sums of two values per thread (the first in 64 bits); returns the totals in ta, tb.
-__device__ __forceinline__ void block_scan2(int64_t& a, int& b, int64_t& ta, int& tb, int64_t* wa, int* wb) {
+// Sums that stay at kMany once they reach it: they are past every limit then, and the order of the additions does not matter.
+constexpr uint32_t kMany = 0x7fffffffu;
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, kMany); }
+
+// Block-wide exclusive sums of two values per thread; the totals in ta, tb.  (Short rolled code: a step runs once, so that
+// what it executes comes through the instruction cache cold.)
+__device__ __forceinline__ void block_scan2(uint32_t& a, uint32_t& b, uint32_t& ta, uint32_t& tb, uint2* warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int64_t ia = a;
-    int ib = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t ya = __shfl_up_sync(kFull, ia, o);
-        const int yb = __shfl_up_sync(kFull, ib, o);
-        if (lane >= o) {
-            ia += ya;
-            ib += yb;
+    uint32_t xa = a, xb = b;
+    uint32_t ia = 0, ib = 0, ca = 0, cb = 0;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {  // within the warp, then over the warps' sums
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t ya = __shfl_up_sync(kFull, xa, o), yb = __shfl_up_sync(kFull, xb, o);
+            if (lane >= o) {
+                xa = add_sat(xa, ya);
+                xb = add_sat(xb, yb);
+            }
+        }
+        if (level == 0) {
+            ia = __shfl_up_sync(kFull, xa, 1);
+            ib = __shfl_up_sync(kFull, xb, 1);
+            if (lane == 0) ia = ib = 0;
+            if (lane == 31) warps[warp] = make_uint2(xa, xb);
+            __syncthreads();
+            const uint2 w = lane < nw ? warps[lane] : make_uint2(0u, 0u);
+            xa = w.x;
+            xb = w.y;
         }
     }
-    if (lane == 31) {
-        wa[warp] = ia;
-        wb[warp] = ib;
-    }
-    __syncthreads();
-    int64_t ca = lane < nw ? wa[lane] : 0;
-    int cb = lane < nw ? wb[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t ya = __shfl_up_sync(kFull, ca, o);
-        const int yb = __shfl_up_sync(kFull, cb, o);
-        if (lane >= o) {
-            ca += ya;
-            cb += yb;
-        }
-    }
-    ta = __shfl_sync(kFull, ca, 31);
-    tb = __shfl_sync(kFull, cb, 31);
-    const int64_t pa = __shfl_sync(kFull, ca, warp == 0 ? 0 : warp - 1);
-    const int pb = __shfl_sync(kFull, cb, warp == 0 ? 0 : warp - 1);
-    a = ia - a + (warp ? pa : 0);
-    b = ib - b + (warp ? pb : 0);
+    ta = __shfl_sync(kFull, xa, 31);
+    tb = __shfl_sync(kFull, xb, 31);
+    ca = __shfl_sync(kFull, xa, max(0, warp - 1));
+    cb = __shfl_sync(kFull, xb, max(0, warp - 1));
+    a = warp ? add_sat(ca, ia) : ia;
+    b = warp ? add_sat(cb, ib) : ib;
 }
 
 // Largest s in [0, n) with P[s] <= x (P[0] = 0 <= x, P non-decreasing).
 __device__ __forceinline__ int find_run(const int* P, int n, int x) {
     int lo = 0, hi = n - 1;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (P[mid] <= x) lo = mid; else hi = mid - 1;
@@ -68,7 +70,7 @@ __device__ __forceinline__ int find_run(const int* P, int n, int x) {
     return lo;
 }
 
-constexpr int kRun = 4;  // consecutive items per thread: one search serves them
+constexpr int kRun = 4;  // consecutive runs of 32 slots per warp: neighbours are mostly the same sequence's
 
 }  // namespace
 
@@ -78,19 +80,18 @@ struct ExtendScan {
     bool ok;
 };
 __device__ __forceinline__ ExtendScan scan_extend(const ExtendArgs& a, int* tok, int* blk, int* past, bool report) {
-    __shared__ int64_t wa[32];
-    __shared__ int wb[32];
+    __shared__ uint2 warps[32];
     const int tid = threadIdx.x, N = a.N, mask = (1 << a.shift) - 1;
     const int per = (N + blockDim.x - 1) / blockDim.x;
     const int lo = min(tid * per, N), hi = min(lo + per, N);
     const int F = *a.free_count;
-    const int64_t cap = static_cast<int64_t>(a.MB) << a.shift;
-    int64_t nt = 0;
-    int nb = 0;
+    const int cap = a.MB << a.shift;
+    uint32_t nt = 0, nb = 0;
     bool bad = false;
+#pragma unroll 1
     for (int s = lo; s < hi; ++s) {
         const int L = a.past_lens[s], n = a.new_lens[s];
-        if (L < 0 || n < 0 || static_cast<int64_t>(L) + n > cap) {
+        if (L < 0 || n < 0 || L > cap || n > cap - L) {
             bad = true;
             continue;
         }
@@ -98,36 +99,37 @@ __device__ __forceinline__ ExtendScan scan_extend(const ExtendArgs& a, int* tok,
         past[s] = L;
         tok[s] = n;
         blk[s] = e;
-        nt += n;
-        nb += e;
+        nt = add_sat(nt, n);
+        nb = add_sat(nb, e);
     }
-    int64_t total_t;
-    int total_b;
-    block_scan2(nt, nb, total_t, total_b, wa, wb);
+    uint32_t total_t, total_b;
+    block_scan2(nt, nb, total_t, total_b, warps);
     bad = __syncthreads_or(bad);
-    const bool no_room = F < 0 || F > a.NB || total_b > F;
-    const bool ok = !bad && !no_room && total_t <= a.max_tokens;
+    const bool no_room = F < 0 || F > a.NB || total_b > static_cast<uint32_t>(F);
+    const bool ok = !bad && !no_room && total_t <= static_cast<uint32_t>(a.max_tokens);
     if (ok) {
+#pragma unroll 1
         for (int s = lo; s < hi; ++s) {
             const int n = tok[s], e = blk[s];
             tok[s] = static_cast<int>(nt);
-            blk[s] = nb;
+            blk[s] = static_cast<int>(nb);
             nt += n;
             nb += e;
         }
         if (tid == 0) {
             tok[N] = static_cast<int>(total_t);
-            blk[N] = total_b;
+            blk[N] = static_cast<int>(total_b);
         }
     } else if (report && tid == 0) {
-        raise_error(a.err, (bad || total_t > a.max_tokens ? PKV_DEVERR_BAD_LENGTH : 0) | (no_room ? PKV_DEVERR_BAD_SLOT : 0));
+        raise_error(a.err, (bad || total_t > static_cast<uint32_t>(a.max_tokens) ? PKV_DEVERR_BAD_LENGTH : 0) | (no_room ? PKV_DEVERR_BAD_SLOT : 0));
     }
     __syncthreads();
-    return {F, ok ? static_cast<int>(total_t) : 0, ok ? total_b : 0, ok};
+    return {F, ok ? static_cast<int>(total_t) : 0, ok ? static_cast<int>(total_b) : 0, ok};
 }
 
 // The lengths and the free count after the step, in place perhaps: for a CTA after which nobody reads the old ones.
 __device__ __forceinline__ void write_extend_state(const ExtendArgs& a, const ExtendScan& r, const int* tok, const int* past) {
+#pragma unroll 1
     for (int s = threadIdx.x; s < a.N; s += blockDim.x)
         a.seq_lens[s] = r.ok ? past[s] + (tok[s + 1] - tok[s]) : a.past_lens[s];  // a refused step leaves them
     if (threadIdx.x == 0) *a.new_free_count = r.F - r.E;
@@ -149,25 +151,24 @@ __global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs
         const int id = __ldg(a.free_blocks + (F - 1 - e));
         return id >= 0 && id < a.NB ? id : -1;
     };
+#pragma unroll 1
     for (int e = at; e < E; e += width) {
         const int s = find_run(blk, N, e);
         const int id = free_id(e);
         if (id < 0) raise_error(a.err, PKV_DEVERR_BAD_BLOCK);
         a.tables[static_cast<size_t>(s) * a.MB + ((past[s] + mask) >> a.shift) + (e - blk[s])] = id;
     }
-    for (int64_t i = static_cast<int64_t>(at) * kRun; i < a.max_tokens; i += static_cast<int64_t>(width) * kRun) {
-        const int t0 = static_cast<int>(i);
-        int s = t0 < T ? find_run(tok, N, t0) : N;
-        int64_t out[kRun];
-        int j_seen = -1, s_seen = -1, id = -1;
-#pragma unroll
-        for (int u = 0; u < kRun; ++u) {
-            const int t = t0 + u;
-            out[u] = -1;
-            if (t >= T) continue;
-            while (tok[s + 1] <= t) ++s;  // tok[N] = T > t
-            const int L = past[s], p = L + t - tok[s], j = p >> a.shift, j_new = (L + mask) >> a.shift;
-            if (j != j_seen || s != s_seen) {  // a block's first token here
+    const int lane = tid & 31;
+#pragma unroll 1
+    for (int64_t i = static_cast<int64_t>(at >> 5) * (32 * kRun); i < a.max_tokens; i += static_cast<int64_t>(width) * kRun) {
+        int s = -1;
+#pragma unroll 1
+        for (int t = static_cast<int>(i) + lane, u = 0; u < kRun && t < a.max_tokens; ++u, t += 32) {
+            int64_t slot = -1;
+            if (t < T) {
+                if (s < 0 || tok[s + 1] <= t) s = find_run(tok, N, t);
+                const int L = past[s], p = L + t - tok[s], j = p >> a.shift, j_new = (L + mask) >> a.shift;
+                int id;
                 if (j >= j_new) {
                     id = free_id(blk[s] + j - j_new);
                 } else {
@@ -177,23 +178,14 @@ __global__ void __launch_bounds__(1024) extend_sequences_kernel(const ExtendArgs
                         raise_error(a.err, PKV_DEVERR_BAD_BLOCK);
                     }
                 }
-                j_seen = j;
-                s_seen = s;
+                if (id >= 0) slot = (static_cast<int64_t>(id) << a.shift) + (p & mask);
             }
-            if (id >= 0) out[u] = (static_cast<int64_t>(id) << a.shift) + (p & mask);
-        }
-        if (t0 + kRun <= a.max_tokens && (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0) {
-#pragma unroll
-            for (int u = 0; u < kRun; u += 2)
-                *reinterpret_cast<longlong2*>(a.slots + t0 + u) = make_longlong2(out[u], out[u + 1]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < kRun; ++u)
-                if (t0 + u < a.max_tokens) a.slots[t0 + u] = out[u];
+            a.slots[t] = slot;
         }
     }
 
     // ---- the step's index arrays, and its state
+#pragma unroll 1
     for (int s = at; s <= N; s += width) {
         if (a.cu_q) a.cu_q[s] = r.ok ? tok[s] : 0;
         if (a.q_starts && s < N) a.q_starts[s] = r.ok ? past[s] : a.past_lens[s];
@@ -217,16 +209,15 @@ struct ReleaseScan {
     bool ok;
 };
 __device__ __forceinline__ ReleaseScan scan_release(const ReleaseArgs& a, int* blk, int* len, bool report) {
-    __shared__ int64_t wa[32];
-    __shared__ int wb[32];
+    __shared__ uint2 warps[32];
     const int tid = threadIdx.x, N = a.N, mask = (1 << a.shift) - 1;
     const int per = (N + blockDim.x - 1) / blockDim.x;
     const int lo = min(tid * per, N), hi = min(lo + per, N);
     const int F = *a.free_count;
-    const int64_t cap = static_cast<int64_t>(a.MB) << a.shift;
-    int64_t n = 0;
-    int none = 0;
+    const int cap = a.MB << a.shift;
+    uint32_t n = 0, none = 0;
     bool bad = false;
+#pragma unroll 1
     for (int s = lo; s < hi; ++s) {
         const int L = a.past_lens[s], k = a.keep_blocks ? a.keep_blocks[s] : 0;
         const bool done = a.finished[s] != 0;
@@ -236,15 +227,15 @@ __device__ __forceinline__ ReleaseScan scan_release(const ReleaseArgs& a, int* b
         }
         len[s] = done ? 0 : L;
         blk[s] = done ? max(0, ((L + mask) >> a.shift) - k) : 0;
-        n += blk[s];
+        n = add_sat(n, blk[s]);
     }
-    int64_t total;
-    int zero;
-    block_scan2(n, none, total, zero, wa, wb);
+    uint32_t total, zero;
+    block_scan2(n, none, total, zero, warps);
     bad = __syncthreads_or(bad);
-    const bool no_room = F < 0 || F > a.NB || total > a.NB - F;
+    const bool no_room = F < 0 || F > a.NB || total > static_cast<uint32_t>(a.NB - F);
     const bool ok = !bad && !no_room;
     if (ok) {
+#pragma unroll 1
         for (int s = lo; s < hi; ++s) {
             const int e = blk[s];
             blk[s] = static_cast<int>(n);
@@ -259,6 +250,7 @@ __device__ __forceinline__ ReleaseScan scan_release(const ReleaseArgs& a, int* b
 }
 
 __device__ __forceinline__ void write_release_state(const ReleaseArgs& a, const ReleaseScan& r, const int* len) {
+#pragma unroll 1
     for (int s = threadIdx.x; s < a.N; s += blockDim.x) a.seq_lens[s] = r.ok ? len[s] : a.past_lens[s];
     if (threadIdx.x == 0) *a.new_free_count = r.F + r.E;
 }
@@ -270,6 +262,7 @@ __global__ void __launch_bounds__(1024) release_sequences_kernel(const ReleaseAr
     const int width = static_cast<int>(gridDim.x * blockDim.x), at = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const ReleaseScan r = scan_release(a, blk, len, blockIdx.x == 0);
+#pragma unroll 1
     for (int e = at; e < r.E; e += width) {
         const int s = find_run(blk, a.N, e);
         const int k = a.keep_blocks ? __ldg(a.keep_blocks + s) : 0;
