@@ -22,7 +22,7 @@
 //     one for both groups' P V, tried first, took 1044 cycles per issue (waits, loop and issue in turn), 2090 per key tile
 //     of two query tiles, with the tensor pipe busy for 1300 of them;
 //   * warps 8 and 10: copy the K and V tiles (TMA, one block of the block table per copy, one lane per block);
-//   * INT8 caches: warps 12-15 widen the codes to f16, two warps per operand, half of the rows each.
+//   * INT8 caches: warps 16-19 widen the codes to f16, two warps per operand, half of the rows each.
 // Hand-offs are mbarriers; every wait is bounded.  On a timeout a role records the error and does nothing more, the CTA
 // drains its own MMAs and copies (bounded) and frees TMEM.
 #include <algorithm>
@@ -49,9 +49,10 @@ struct FullPlan {
     static constexpr int kOffV = kOffK + kStages * kStage;
     static constexpr int kOffStg = kOffV + kStages * kStage;
     static constexpr int kOffMeta = kOffStg + 2 * kSlots * kStgSlot;
-    static constexpr int kThreads = 512;
-    // registers per thread after the split: 256 x 184 + 256 x 72 = 512 x 128, what the launch gives
-    static constexpr int kRegsSoftmax = 184, kRegsOther = 72;
+    static constexpr int kThreads = NARROW == 2 ? 640 : 512;
+    // registers per thread after the split: 256 x 184 + 256 x 72 = 512 x 128, what the launch gives;
+    // 256 x 168 + 384 x 48 = 640 x 96
+    static constexpr int kRegsSoftmax = NARROW == 2 ? 168 : 184, kRegsOther = NARROW == 2 ? 48 : 72;
 };
 
 // mbarriers
@@ -65,10 +66,10 @@ constexpr int kFDrain = 57;
 constexpr int kFStg = 58, kFStgFree = 66;           // + 4 * (V ? 1 : 0) + slot
 constexpr int kFBars = 74;
 constexpr int kFTmem = 8 * kFBars, kFAbort = kFTmem + 4;  // byte offsets
-constexpr int kFPart = kFAbort + 4;                 // per-warp sums of the plan's scan
-constexpr int kFMine = kFPart + 64;                 // ints: x0, x1; the lister's chunk, item, first unit; items listed, more,
-                                                    // nothing listed yet; + group: the V stage whose rows are to be zeroed
-constexpr int kFItems = 720;
+constexpr int kFPart = kFAbort + 4;                 // per-warp sums of the plan's scan: units [32], items [32]
+constexpr int kFMine = kFPart + 256;                // ints: x0, x1; the lister's chunk, item, first unit; items listed, more,
+                                                    // the first item's index; + group: the V stage with rows to be zeroed
+constexpr int kFItems = 912;
 constexpr int kFMlOut = kFItems + 32 * kBatch;      // (m, l) of the other group's rows, [owner][128]
 constexpr int kFUnits = kFMlOut + 2 * 128 * 8;      // the chunks' first units, [kMaxSeqs]
 constexpr int kFEnd = kFUnits + 4 * kMaxSeqs;
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         if (i >= kFMl && i <= kFZero) count = 128;
         if ((i >= kFKEmpty && i < kFVFull) || (i >= kFVEmpty && i < kFS)) count = 2;
         if (i == kFDrain) count = 4;
+        if (NARROW == 2 && (i < kFKEmpty || (i >= kFVFull && i < kFVEmpty) || i >= kFStgFree)) count = 2;
         mbar_init(bar + 8 * i, count);
         fence_mbar_init();
     }
@@ -172,68 +174,120 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         k.items = k.kt > 0 ? ((k.tokens + cta_q - 1) >> cta_shift) * a.Hkv : 0;
         return k;
     };
-    int share;
+    // Part of item m (KV head and query tiles) of a chunk whose first unit is `start`, into the list.
+    auto put_item = [&](int slot, const Chunk& k, int start, int m, bool first) {
+        const int x0 = mine[0], x1 = mine[1], tile = m / a.Hkv, h = m - tile * a.Hkv, t0 = tile << cta_shift;
+        const int Uk = start + m * k.ku, j0 = max(0, x0 - Uk - kItemUnits) >> (k.w - 1);
+        Item it;
+        it.q_row = k.q0 + t0;
+        it.tokens = min(cta_q, k.tokens - t0);
+        it.keys = k.keys;
+        it.table = k.table;
+        it.j0 = j0;
+        it.n = min(k.kt, (min(Uk + k.ku, x1) - Uk - kItemUnits) >> (k.w - 1)) - j0;
+        it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
+        it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
+        items[slot] = it;
+        if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk, Uk + k.ku) : make_int4(0, 0, 0, 0);
+    };
+    // Items of a chunk that start before x1, but the last of them if x1 is among its first units.
+    auto items_before = [&](const Chunk& k, int start, int x1) {
+        return k.items == 0 || start + kItemUnits >= x1 ? 0 : min(k.items, ceil_div(x1 - start - kItemUnits, k.ku));
+    };
+    // Each thread takes a contiguous run of chunks: (0) the sums of their units and items; (1) with what comes before
+    // known, the place where this CTA's share starts; (2) the first batch of its items.
     {
-        // stream units per chunk and their prefix: each thread takes a contiguous run of chunks
         const int per = ceil_div(n_chunks, kNT);
         const int c_lo = min(tid * per, n_chunks), c_hi = min(c_lo + per, n_chunks);
-        int sum = 0, run = 0, x0 = 0, x1 = 0;
-        share = 0;
+        int sum = 0, count = 0, before = 0, items_at = 0, x0 = 0, x1 = 0;  // units and items; of the chunks before this thread's
+        Chunk k = {};
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {  // the sums; then, with what comes before known, this CTA's place
+        for (int pass = 0; pass < 3; ++pass) {
+            int run = before, index = items_at;
 #pragma unroll 1
             for (int c = c_lo; c < c_hi; ++c) {
-                const Chunk k = load_chunk(c, pass == 0 && cta == 0);
+                if (pass == 0 || per > 1) k = load_chunk(c, pass == 0 && cta == 0);
                 const int units = k.items * k.ku;
                 if (pass == 0) {
                     sum += units;
-                    continue;
+                    count += k.items;
+                } else if (pass == 1) {
+                    first_unit[c] = run;
+                    if (run <= x0 && x0 < run + units && x0 < x1) {  // where this CTA starts
+                        const int m = (x0 - run) / k.ku;
+                        mine[2] = c;
+                        mine[3] = m;
+                        mine[4] = run;
+                        mine[7] = index + m;
+                    }
+                } else if (run + units > x0 && run < x1) {
+                    const int m0 = max(0, mine[7] - index), m1 = items_before(k, run, x1), slot0 = index - mine[7];
+                    const int m2 = min(m1, kBatch - slot0);
+#pragma unroll 1
+                    for (int m = m0; m < m2; ++m) put_item(slot0 + m, k, run, m, slot0 + m == 0);
+                    if (m2 > m0) atomicMax(const_cast<int*>(mine) + 5, slot0 + m2);
+                    if (m1 > m2 && m2 >= m0 && slot0 + m0 <= kBatch) {  // the list is full: the next batch starts here
+                        mine[2] = c;
+                        mine[3] = m2;
+                        mine[4] = run;
+                        mine[6] = 1;
+                    }
                 }
-                if (run <= x0 && x0 < run + units && x0 < x1) {  // where this CTA starts
-                    mine[2] = c;
-                    mine[3] = (x0 - run) / k.ku;
-                    mine[4] = run;
-                }
-                first_unit[c] = run;
                 run += units;
+                index += k.items;
             }
-            if (pass == 1) break;
-            int incl = sum;
+            if (pass == 2) break;
+            if (pass == 1) {
+                __syncthreads();
+                continue;
+            }
+            int iu = sum, ic = count;
 #pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (lane == 31) part[warp] = incl;
-            tc_fence_before();
-            __syncthreads();
-            tc_fence_after();
-            int before = lane < kNT / 32 ? part[lane] : 0;  // of the warps up to lane's
+            for (int level = 0; level < 2; ++level) {  // within the warp, then over the warps' sums
 #pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, before, o);
-                if (lane >= o) before += y;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int yu = __shfl_up_sync(kFull, iu, o), yc = __shfl_up_sync(kFull, ic, o);
+                    if (lane >= o) {
+                        iu += yu;
+                        ic += yc;
+                    }
+                }
+                if (level == 1) break;
+                before = iu - sum;
+                items_at = ic - count;
+                if (lane == 31) {
+                    part[warp] = iu;
+                    part[32 + warp] = ic;
+                }
+                tc_fence_before();
+                __syncthreads();
+                tc_fence_after();
+                iu = lane < kNT / 32 ? part[lane] : 0;
+                ic = lane < kNT / 32 ? part[32 + lane] : 0;
             }
-            const int T = __shfl_sync(kFull, before, 31), mine_before = __shfl_sync(kFull, before, max(0, warp - 1));
-            run = incl - sum + (warp ? mine_before : 0);
-            share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
+            const int T = __shfl_sync(kFull, iu, 31), bu = __shfl_sync(kFull, iu, max(0, warp - 1));
+            const int bc = __shfl_sync(kFull, ic, max(0, warp - 1));
+            if (warp) {
+                before += bu;
+                items_at += bc;
+            }
+            const int share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
             x0 = static_cast<int>(min(static_cast<int64_t>(cta) * share, static_cast<int64_t>(T)));
             x1 = static_cast<int>(min(static_cast<int64_t>(x0) + share, static_cast<int64_t>(T)));
             if (tid == 0) {
                 mine[0] = x0;
                 mine[1] = x1;
-                mine[7] = 1;  // nothing listed yet
-                if (x0 >= x1) mine[2] = n_chunks;
+                mine[5] = mine[6] = 0;
                 if (cta == ncta - 1) *f.share = share;
+                f.cuts[cta] = make_int4(0, 0, 0, 0);
             }
         }
     }
-    __syncthreads();
     const uint32_t tmem = *tmem_slot;
 
     // The next batch of this CTA's items, by one warp: 32 chunks at a time, a lane each.
     auto list_items = [&]() {
-        const int x0 = mine[0], x1 = mine[1], listed_none = mine[7];
+        const int x1 = mine[1];
         int c0 = mine[2], k0 = mine[3], U = mine[4], n = 0, more = 0;
         __syncwarp();
 #pragma unroll 1
@@ -248,10 +302,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 const int y = __shfl_up_sync(kFull, iu, o);
                 if (lane >= o) iu += y;
             }
-            const int start = U + iu - units, k_lo = lane == 0 ? k0 : 0;
-            // the items that start before x1, but the last of them if x1 is among its first units
-            const int k_hi = k.items == 0 || start + kItemUnits >= x1 ? 0 : min(k.items, ceil_div(x1 - start - kItemUnits, k.ku));
-            const int cnt = max(0, k_hi - k_lo);
+            const int start = U + iu - units, k_lo = lane == 0 ? k0 : 0, cnt = max(0, items_before(k, start, x1) - k_lo);
             int ic = cnt;
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
@@ -260,23 +311,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             }
             const int pos = n + ic - cnt, fits = min(cnt, max(0, kBatch - pos)), total = __shfl_sync(kFull, ic, 31);
 #pragma unroll 1
-            for (int i = 0; i < fits; ++i) {
-                const int m = k_lo + i, h = m % a.Hkv, t0 = (m / a.Hkv) * cta_q, Uk = start + m * k.ku;
-                const int j0 = max(0, x0 - Uk - kItemUnits) >> (k.w - 1);
-                const int j1 = min(k.kt, (min(Uk + k.ku, x1) - Uk - kItemUnits) >> (k.w - 1));
-                Item it;
-                it.q_row = k.q0 + t0;
-                it.tokens = min(cta_q, k.tokens - t0);
-                it.keys = k.keys;
-                it.table = k.table;
-                it.j0 = j0;
-                it.n = j1 - j0;
-                it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
-                it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
-                items[pos + i] = it;
-                if (listed_none && pos + i == 0)
-                    f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk, Uk + k.ku) : make_int4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < fits; ++i) put_item(pos + i, k, start, k_lo + i, false);
             if (n + total > kBatch) {  // the first lane whose items do not all fit is where the next batch starts
                 const unsigned over = __ballot_sync(kFull, pos + cnt > kBatch);
                 if (lane == __ffs(over) - 1) {
@@ -294,25 +329,25 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             k0 = 0;
         }
         if (lane == 0) {
-            if (listed_none && n == 0) f.cuts[cta] = make_int4(0, 0, 0, 0);
             mine[5] = n;
             mine[6] = more;
-            mine[7] = 0;
         }
         __syncwarp();
     };
     // Every role runs its body once per batch of listed items.
     auto batches = [&](auto lister, auto&& body) {
-        int more;
-        do {
+        __syncthreads();  // the first batch is listed
+#pragma unroll 1
+        while (true) {
+            const int more = mine[6];
+            body(mine[5]);
+            if (!more) break;
             __syncthreads();
             if constexpr (decltype(lister)::value) {
                 if (warp == 9) list_items();
             }
             __syncthreads();
-            more = mine[6];
-            body(mine[5]);
-        } while (more);
+        }
     };
 
     // ---- what the joining needs to know of each sequence, and the rows without keys: from the last CTA down, the first
@@ -519,12 +554,13 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     }
                 }
             });
-        } else if (NARROW == 2 && (warp == 12 || warp == 14)) {
-            // ------------------------------------------------ INT8: every K (warp 12) or V tile (14) from its staging slot
-            // into the f16 ring, exactly (the scales go to the scores and the output); rows lane and 32 + lane
+        } else if (NARROW == 2 && warp >= 16) {
+            // ------------------------------------------------ INT8: rows 32 half + lane of every K (warps 16, 18) or V tile
+            // (17, 19) from its staging slot into the f16 ring, exactly (the scales go to the scores and the output).  With
+            // one warp per operand a key tile took 2300 cycles, whatever else was done with it.
             constexpr int kSlots = PL::kSlots ? PL::kSlots : 1;
-            const bool is_v = warp == 14;
-            const int sw = lane & 7;
+            const bool is_v = warp & 1;
+            const int r = lane + 32 * (warp >= 18), sw = r & 7;
             const int full = is_v ? kFVFull : kFKFull, empty = is_v ? kFVEmpty : kFKEmpty;
             int g = 0;
             batches(std::false_type{}, [&](int n) {
@@ -537,12 +573,11 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         ok = warp_wait(bar + 8 * (kFStg + 4 * is_v + slot), (g / kSlots) & 1, a.timeout_ns) &&
                              (g < kStages || warp_wait(bar + 8 * (empty + st), (g / kStages - 1) & 1, a.timeout_ns));
                         if (!ok) break;
-                        const uint8_t* src = smem + PL::kOffStg + (is_v * PL::kSlots + slot) * kStgSlot + lane * 128;
-                        uint8_t* dst = smem + (is_v ? PL::kOffV : PL::kOffK) + st * kStage + lane * 128;
-#pragma unroll 8
-                        for (int k = 0; k < 16; ++k) {  // 16 codes: head dims 16 (k & 7) .. + 15 of row lane + 32 (k >> 3)
-                            const int c16 = k & 7, ro = (k >> 3) * 32 * 128;
-                            const uint4 wv = *reinterpret_cast<const uint4*>(src + ro + ((c16 ^ sw) * 16));
+                        const uint8_t* src = smem + PL::kOffStg + (is_v * PL::kSlots + slot) * kStgSlot + r * 128;
+                        uint8_t* dst = smem + (is_v ? PL::kOffV : PL::kOffK) + st * kStage + r * 128;
+#pragma unroll 4
+                        for (int k = 0; k < 8; ++k) {  // 16 codes: head dims 16 k .. 16 k + 15
+                            const uint4 wv = *reinterpret_cast<const uint4*>(src + ((k ^ sw) * 16));
                             const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
                             uint32_t o[8];
 #pragma unroll
@@ -551,8 +586,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                                 o[2 * u] = s8x2_to_f16x2(fl, 0);
                                 o[2 * u + 1] = s8x2_to_f16x2(fl, 2);
                             }
-                            uint8_t* dh = dst + ro + (c16 >> 2) * kKvHalf;
-                            const int lc = 2 * (c16 & 3);
+                            uint8_t* dh = dst + (k >> 2) * kKvHalf;
+                            const int lc = 2 * (k & 3);
                             *reinterpret_cast<uint4*>(dh + ((lc ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
                             *reinterpret_cast<uint4*>(dh + (((lc + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
@@ -792,7 +827,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
     // ---- drain: nothing of this CTA may still be in flight when TMEM is freed and the CTA exits
     __syncthreads();
-    if (warp >= 8 && (warp & 1) && *abort_flag) {
+    if (warp >= 8 && warp < 16 && (warp & 1) && *abort_flag) {
         tc_commit_warp(bar + 8 * kFDrain);  // arrives once every MMA this warp issued has completed
         mbar_wait_bounded(bar + 8 * kFDrain, 0, a.timeout_ns);
     }
