@@ -469,9 +469,11 @@ pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t max_blocks
  *                [cu_groups[g], cu_groups[g + 1]); every sequence is in one group.
  *   prefix_lens: [num_groups] device int32: tokens shared by the whole group, a
  *                multiple of block_size (only full blocks are shared), 0 for none,
- *                and no more than the context length of any of its sequences.
- * The prefix is read through the table row of the group's first sequence; the
- * other rows' first prefix_lens / block_size entries are not read.
+ *                and no more than the context length of any of its sequences but
+ *                those of length 0 (finished, padding), whose rows are zero.
+ * The prefix is read through the table row of the group's first sequence, of
+ * whatever length that is; the other rows' first prefix_lens / block_size entries
+ * are not read.
  * A sequence whose group or lengths break these rules sets PKV_DEVERR_BAD_LENGTH;
  * its row is zero, or undefined where the group's own sizes are malformed.
  *   workspace: >= pkv_paged_attention_decode_prefix_workspace_size bytes, 16-byte
@@ -480,7 +482,8 @@ pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t max_blocks
  * pkv_paged_attention_decode_shared (per cache type), both in fp32 sums.
  * Supported: bf16 queries, bf16, FP8 or INT8 cache, head_dim 128, block_size
  *   8/16/32, G in {1, 2, 4, 8}, num_seqs <= 8192, num_groups <= 2048, scale
- *   positive.  Two kernels, the second launched while the first runs.
+ *   positive.  Four kernels (operands and counters, prefixes, own blocks, joining),
+ *   each launched while the one before it runs.
  */
 pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, int32_t q_dtype, const void* k_cache,
                                              const void* v_cache, const pkv_cache_desc* cache,

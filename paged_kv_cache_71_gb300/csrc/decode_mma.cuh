@@ -206,8 +206,8 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
             if constexpr (PREFIX) {
                 while (grp + 1 < px.num_groups && px.cu_groups[grp + 1] <= s) ++grp;
                 const int g0 = px.cu_groups[grp], g1 = px.cu_groups[grp + 1], p = px.prefix_lens[grp];
-                bad = bad || g0 < 0 || g0 > s || g1 <= s || g1 > B || p < 0 || p % S != 0 || p > L;
-                skip = bad ? 0 : p / S;
+                bad = bad || g0 < 0 || g0 > s || g1 <= s || g1 > B || p < 0 || p % S != 0 || (p > L && L != 0);
+                skip = bad || L == 0 ? 0 : p / S;  // L = 0: no sequence in this row
                 P[B + 1 + s] = bad ? -1 : skip;
                 if (s % ncta == cta) px.prefix_blocks[s] = P[B + 1 + s];
             }
