@@ -106,6 +106,39 @@ class SequenceTables:
             out[i, : len(r)] = r
         return out
 
+    def prefix_groups(self, sids) -> tuple[np.ndarray, np.ndarray]:
+        """The batch's shared prefixes as ``pkv_paged_attention_decode_prefix`` takes them: int32 ``cu_groups`` and
+        ``prefix_lens``, for rows in the order of ``sids``.
+
+        Neighbours whose tables start with the same full blocks are a group, so forks of one sequence and requests over
+        one document should stand side by side in a batch.  A group of n over p blocks saves (n - 1) * p block reads;
+        the next sequence joins it if the n + 1 of them over the c blocks that they all share save as many or more:
+        n * c >= (n - 1) * p.  A group of one shares nothing: prefix 0.
+        """
+        cu, lens = [0], []
+        shared: list = []                                # the open group's common full blocks
+        n = 0
+
+        def close():
+            cu.append(cu[-1] + n)
+            lens.append(len(shared) * self.block_size if n > 1 else 0)
+
+        for sid in sids:
+            seq = self._seqs[sid]
+            full = seq.blocks[: seq.length // self.block_size]
+            c = 0
+            while c < min(len(full), len(shared)) and full[c] == shared[c]:
+                c += 1
+            if c and n * c >= (n - 1) * len(shared):
+                shared, n = shared[:c], n + 1
+                continue
+            if n:
+                close()
+            shared, n = full, 1
+        if n:
+            close()
+        return np.asarray(cu, dtype=np.int32), np.asarray(lens, dtype=np.int32)
+
     # ---- changes
     def prefill(self, sid, n_tokens: int) -> None:
         """A new sequence holding n_tokens tokens: ceil(n / S) fresh blocks."""

@@ -6,6 +6,7 @@ import torch
 
 import paged_kv_cache_71_gb300 as pkv
 from paged_kv_cache_71_gb300 import _binding as B
+from paged_kv_cache_71_gb300.block_manager import SequenceTables
 
 
 def _desc(**kw):
@@ -171,3 +172,49 @@ def test_the_calls_fail_loudly_without_the_library(monkeypatch, tmp_path):
         pkv.pkv_extend_sequences(_z(2, 4), _z(2), _z(2), 16, _z(8), _z(1), _z(2), _z(1), _z(8, dtype=torch.int64))
     with pytest.raises(RuntimeError, match="not built"):
         pkv.pkv_paged_cross_attention_workspace_size(_desc(), 4, 2, 32)
+
+
+def _tables(lengths, forks=()):
+    tabs = SequenceTables(64, 4)
+    for sid, n in lengths.items():
+        tabs.prefill(sid, n)
+    for parent, child, own in forks:
+        tabs.fork(parent, child)
+        for _ in range(own):
+            tabs.next_slot(child)
+    return tabs
+
+
+def test_prefix_groups_of_the_block_manager():
+    """Forks of two sequences beside sequences of their own; the partly filled block is no one's prefix."""
+    tabs = _tables({"a": 10, "b": 9, "c": 3}, [("a", "a1", 5), ("a", "a2", 0), ("b", "b1", 2)])
+    cu, pre = tabs.prefix_groups(["a", "a1", "a2", "b", "b1", "c"])
+    assert cu.tolist() == [0, 3, 5, 6] and pre.tolist() == [8, 8, 0]
+    assert cu.dtype == pre.dtype == "int32"
+    cu, pre = tabs.prefix_groups(["c", "a", "b", "a1"])      # apart from one another they share nothing
+    assert cu.tolist() == [0, 1, 2, 3, 4] and pre.tolist() == [0, 0, 0, 0]
+    cu, pre = tabs.prefix_groups([])
+    assert cu.tolist() == [0] and pre.tolist() == []
+
+
+def test_prefix_groups_keep_the_larger_saving():
+    """Three sequences over 5 blocks save 10 block reads; a fourth over 1 block would leave 3, over 4 blocks 12."""
+    tabs = _tables({"root": 4})
+    tabs.fork("root", "long")
+    for _ in range(16):
+        tabs.next_slot("long")
+    for child in ("x", "y"):
+        tabs.fork("long", child)
+    tabs.fork("root", "short")
+    for _ in range(16):
+        tabs.next_slot("short")
+    cu, pre = tabs.prefix_groups(["long", "x", "y", "short"])
+    assert cu.tolist() == [0, 3, 4] and pre.tolist() == [20, 0]
+    tabs = _tables({"root": 16})
+    for child, own in (("x", 4), ("z", 0)):
+        tabs.fork("root", child)
+        for _ in range(own):
+            tabs.next_slot(child)
+    tabs.fork("x", "y")
+    cu, pre = tabs.prefix_groups(["x", "y", "root", "z"])    # 5 blocks, 5 blocks, then 4 of all three and of all four
+    assert cu.tolist() == [0, 4] and pre.tolist() == [16]
