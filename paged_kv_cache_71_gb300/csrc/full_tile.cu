@@ -5,8 +5,8 @@
 // S = Q K^T, P = 2^(S - m) with the running maximum m (log2 units), O += P V.
 //
 // Work split: the items are laid end to end in units, a key tile that serves two query tiles counting two and one that
-// serves a single one counting one, kItemUnits more for every item, rounded up to an even number, and cut into equal
-// shares, one per CTA (SM); a cut in an item's first kItemUnits falls before it.  An item that is cut, and every item of a
+// serves a single one counting one, item_units more for every item, rounded up to an even number, and cut into equal
+// shares, one per CTA (SM); a cut in an item's first item_units falls before it.  An item that is cut, and every item of a
 // shared prefix, leaves a partial record for each of its pieces; they join as
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i / l
 // in a kernel launched beside this one: join_cuts_kernel (cross attention), join_rows_kernel (shared prefixes).
@@ -36,7 +36,9 @@ namespace {
 
 // Fewest units in a share (even): a piece costs a record and its joining whatever its length.
 constexpr int kMinShare = 8;
-constexpr int kItemUnits = 4;  // what an item costs beside its key tiles
+// What an item costs beside its key tiles, which count w units each (w: query tiles).  4 units for either kind, tried first,
+// left the SMs with many short items of two query tiles behind: 12 prompts over long states took 810 us against 785.
+__device__ constexpr int item_units(int w) { return 4 * w; }
 constexpr int kBatch = 128;    // items that a CTA lists at a time
 
 template <int NARROW>
@@ -170,29 +172,29 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         k.table = (f.prefix ? k.q0 : c) * a.MB;
         k.w = k.tokens > rows_q ? 2 : 1;
         k.kt = (max(k.keys, 0) + kKeys - 1) / kKeys;
-        k.ku = k.kt > 0 ? (k.kt * k.w + kItemUnits + 1) & ~1 : 0;
+        k.ku = k.kt > 0 ? (k.kt * k.w + item_units(k.w) + 1) & ~1 : 0;
         k.items = k.kt > 0 ? ((k.tokens + cta_q - 1) >> cta_shift) * a.Hkv : 0;
         return k;
     };
     // Part of item m (KV head and query tiles) of a chunk whose first unit is `start`, into the list.
     auto put_item = [&](int slot, const Chunk& k, int start, int m, bool first) {
         const int x0 = mine[0], x1 = mine[1], tile = m / a.Hkv, h = m - tile * a.Hkv, t0 = tile << cta_shift;
-        const int Uk = start + m * k.ku, j0 = max(0, x0 - Uk - kItemUnits) >> (k.w - 1);
+        const int Uk = start + m * k.ku, j0 = max(0, x0 - Uk - item_units(k.w)) >> (k.w - 1);
         Item it;
         it.q_row = k.q0 + t0;
         it.tokens = min(cta_q, k.tokens - t0);
         it.keys = k.keys;
         it.table = k.table;
         it.j0 = j0;
-        it.n = min(k.kt, (min(Uk + k.ku, x1) - Uk - kItemUnits) >> (k.w - 1)) - j0;
+        it.n = min(k.kt, (min(Uk + k.ku, x1) - Uk - item_units(k.w)) >> (k.w - 1)) - j0;
         it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
         it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
         items[slot] = it;
-        if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk, Uk + k.ku) : make_int4(0, 0, 0, 0);
+        if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk + item_units(k.w), Uk + k.ku) : make_int4(0, 0, 0, 0);
     };
     // Items of a chunk that start before x1, but the last of them if x1 is among its first units.
     auto items_before = [&](const Chunk& k, int start, int x1) {
-        return k.items == 0 || start + kItemUnits >= x1 ? 0 : min(k.items, ceil_div(x1 - start - kItemUnits, k.ku));
+        return k.items == 0 || start + item_units(k.w) >= x1 ? 0 : min(k.items, ceil_div(x1 - start - item_units(k.w), k.ku));
     };
     // Each thread takes a contiguous run of chunks: (0) the sums of their units and items; (1) with what comes before
     // known, the place where this CTA's share starts; (2) the first batch of its items.
@@ -357,8 +359,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         const Chunk k = load_chunk(s, false);
         if (f.prefix) {
             for (int i = tid; i < k.tokens; i += kNT)
-                f.seq_plan[k.q0 + i] = make_int4(first_unit[s] + (i >> cta_shift) * a.Hkv * k.ku + kItemUnits, k.ku, (i & (cta_q - 1)) << g_shift,
-                                                  k.ku - kItemUnits);
+                f.seq_plan[k.q0 + i] = make_int4(first_unit[s] + (i >> cta_shift) * a.Hkv * k.ku + item_units(k.w), k.ku, (i & (cta_q - 1)) << g_shift,
+                                                  k.ku - item_units(k.w));
         } else if (k.keys == 0) {
             uint4* o = reinterpret_cast<uint4*>(a.out) + static_cast<size_t>(k.q0) * a.Hq * 16;
 #pragma unroll 1
@@ -869,7 +871,7 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const PrefillArgs a, con
     const int4 cut = f.cuts[c];
     const int share = *f.share, U0 = cut.z, U1 = cut.w;
     // the item's first extra piece does it: the cut before it, if any, falls before the item or in its first units
-    if (U1 == 0 || (c - 1) * share - U0 > kItemUnits) return;
+    if (U1 == 0 || (c - 1) * share > U0) return;
     const int valid = (cut.y & 0xffff) * a.G, h = cut.y >> 16, c_last = (U1 - 1) / share;
 #pragma unroll 1
     for (int r = blockIdx.y * 32 + warp; r < min(valid, static_cast<int>(blockIdx.y) * 32 + 32); r += 8) {

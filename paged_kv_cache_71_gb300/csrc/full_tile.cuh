@@ -19,7 +19,7 @@ struct FullArgs {
     const float* q_scale;  // one-byte caches: [rows] of (token, query head), what the operands' scores are multiplied by
     int* share;          // stream units per CTA
     int4* cuts;          // [CTAs] {first token, tokens | head << 16, U0, U1} of the item that the CTA's share starts inside
-                         // of, at units [U0, U1) of the stream; U1 = 0: none
+                         // of, its key tiles at units [U0, U1) of the stream; U1 = 0: none
     int4* seq_plan;      // shared prefixes: [sequences] {first key tile's unit of KV head 0's item, units per item, row in the
                          // item, units of its key tiles}
     const int* prefix_blocks;  // [sequences] as the decode of the own blocks found them: > 0 if the row is to be joined
