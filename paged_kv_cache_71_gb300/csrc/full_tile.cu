@@ -96,6 +96,11 @@ struct Chunk {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Sums of units stop at INT_MAX, which only query ranges that overlap (malformed) can reach: the host bounds the others.
+__device__ __forceinline__ int add_units(int a, int b) {
+    return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
+}
+
 __device__ __forceinline__ void store_v8(float* p, const float* v) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                  "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 if (pass == 0 || per > 1) k = load_chunk(c, pass == 0 && cta == 0);
                 const int units = k.items * k.ku;
                 if (pass == 0) {
-                    sum += units;
+                    sum = add_units(sum, units);
                     count += k.items;
                 } else if (pass == 1) {
                     first_unit[c] = run;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         mine[4] = run;
                         mine[7] = index + m;
                     }
-                } else if (run + units > x0 && run < x1) {
+                } else if (x0 < x1 && run + units > x0 && run < x1) {
                     const int m0 = max(0, mine[7] - index), m1 = items_before(k, run, x1), slot0 = index - mine[7];
                     const int m2 = min(m1, kBatch - slot0);
 #pragma unroll 1
@@ -250,8 +255,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 for (int o = 1; o < 32; o <<= 1) {
                     const int yu = __shfl_up_sync(kFull, iu, o), yc = __shfl_up_sync(kFull, ic, o);
                     if (lane >= o) {
-                        iu += yu;
-                        ic += yc;
+                        iu = add_units(iu, yu);
+                        ic = add_units(ic, yc);
                     }
                 }
                 if (level == 1) break;
@@ -267,13 +272,20 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 iu = lane < kNT / 32 ? part[lane] : 0;
                 ic = lane < kNT / 32 ? part[32 + lane] : 0;
             }
-            const int T = __shfl_sync(kFull, iu, 31), bu = __shfl_sync(kFull, iu, max(0, warp - 1));
+            int T = __shfl_sync(kFull, iu, 31);
+            const int bu = __shfl_sync(kFull, iu, max(0, warp - 1));
             const int bc = __shfl_sync(kFull, ic, max(0, warp - 1));
             if (warp) {
                 before += bu;
                 items_at += bc;
             }
-            const int share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
+            int share = 0x7fffffff;
+            if (T == 0x7fffffff) {  // nothing is done
+                T = 0;
+                if (cta == 0 && tid == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
+            } else {
+                share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
+            }
             x0 = static_cast<int>(min(static_cast<int64_t>(cta) * share, static_cast<int64_t>(T)));
             x1 = static_cast<int>(min(static_cast<int64_t>(x0) + share, static_cast<int64_t>(T)));
             if (tid == 0) {

@@ -273,3 +273,22 @@ def test_a_query_beyond_f16_is_reported_for_int8():
     b.run()
     torch.cuda.synchronize()
     assert int(b.err) & B.DEVERR_Q_RANGE
+
+
+def test_groups_that_overlap_beyond_what_can_be_counted_are_reported():
+    """Every other group claims the whole batch: 1024 times 32 heads, 64 tiles and 512 key tiles are more units than 32 bits
+    hold.  The prefixes are left out, reported, and nothing is read or written out of place."""
+    n, Hkv, G, S, width = 2048, 32, 8, 8, 4096
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.zeros(2, S, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    desc = pkv.CacheDesc.for_cache(k)
+    tables = torch.zeros(n, width, **i32)
+    lens = torch.full((n,), width * S, **i32)
+    cu = torch.tensor([0, n] * 1024 + [0], **i32)
+    pre = torch.full((2048,), width * S, **i32)
+    q = torch.zeros(n, Hkv * G, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    ws = torch.zeros(pkv.pkv_paged_attention_decode_prefix_workspace_size(desc, n, Hkv * G), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, **i32)
+    pkv.pkv_paged_attention_decode_prefix(out, q, k, k, desc, tables, lens, cu, pre, 0.1, ws, err)
+    assert int(err) & B.DEVERR_BAD_LENGTH
