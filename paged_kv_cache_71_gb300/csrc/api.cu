@@ -1103,11 +1103,11 @@ PKV_API pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t ma
 
 // ------------------------------------------------------------------ attention without a mask: shared prefixes, cross
 
-// Scratch of the unmasked stream (full_tile.cu): the share, the cut items, with prefixes the sequences' plan and prefix
-// blocks, for one-byte caches the queries' operands and scales, then the partial records' (m, l) and O: one row per (query token, query head), with prefixes a second one for the
-// sequences' own blocks, and 256 per CTA.
+// Scratch of the unmasked stream (full_tile.cu): the shares, the cut items, with prefixes the sequences' plan and prefix
+// blocks, for one-byte caches the queries' operands and scales, then the partial records' (m, l) and O: one row per (query
+// token, query head), with prefixes a second one for the sequences' own blocks, and 256 per CTA.
 struct FullScratch {
-    size_t share, cuts, plan, blocks, q_ops, q_scale, ml, o, total;  // byte offsets, and the whole
+    size_t share, points, cuts, plan, blocks, q_ops, q_scale, ml, o, total;  // byte offsets, and the whole
     size_t own_row, extra_row;
 };
 static FullScratch full_scratch(int sms, int tokens, int Hq, int dtype, bool prefix) {
@@ -1117,7 +1117,8 @@ static FullScratch full_scratch(int sms, int tokens, int Hq, int dtype, bool pre
     f.extra_row = f.own_row * (prefix ? 2 : 1);
     const size_t rows = f.extra_row + static_cast<size_t>(sms) * 256;
     f.share = 0;
-    f.cuts = 256;
+    f.points = 256;
+    f.cuts = f.points + up(static_cast<size_t>(sms + 1) * 4);
     f.plan = f.cuts + up(static_cast<size_t>(sms) * 16);
     f.blocks = f.plan + (prefix ? up(static_cast<size_t>(tokens) * 16) : 0);
     f.q_ops = f.blocks + (prefix ? up(static_cast<size_t>(tokens) * 4) : 0);
@@ -1140,6 +1141,7 @@ static FullArgs full_args(const FullScratch& f, void* base, const int32_t* lens,
     a.own_row = static_cast<int64_t>(f.own_row);
     a.extra_row = static_cast<int64_t>(f.extra_row);
     a.share = reinterpret_cast<int*>(p + f.share);
+    a.points = reinterpret_cast<int*>(p + f.points);
     a.cuts = reinterpret_cast<int4*>(p + f.cuts);
     a.seq_plan = num_seqs ? reinterpret_cast<int4*>(p + f.plan) : nullptr;
     a.prefix_blocks = reinterpret_cast<int*>(p + f.blocks);
@@ -1234,7 +1236,7 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix_workspace_size(const pkv_ca
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
     if (!bytes) return fail(PKV_ERR_INVALID_ARG, "bytes is NULL");
-    if (num_seqs < 0 || num_q_heads <= 0) 
+    if (num_seqs < 0 || num_q_heads <= 0)
         return fail(PKV_ERR_INVALID_ARG, "bad sizes (num_seqs=%d num_q_heads=%d)", num_seqs, num_q_heads);
     int G;
     if ((st = check_full("the shared-prefix decode", PKV_BF16, *cache, num_q_heads, 8, &G)) != PKV_OK) return st;

@@ -11,20 +11,29 @@
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  O = sum 2^(m_i - M) O_i / l
 // in a kernel launched beside this one: join_cuts_kernel (cross attention), join_rows_kernel (shared prefixes).
 //
+// (Cross attention with many long items: whole items in rounds first, see kRounds.)
+//
 // A CTA runs its share as one stream: TMEM, barriers and the K/V rings live through all of its items, and the copies of
-// the next item's keys run while the current one ends.  Two groups, A and B (128 softmax threads, one per query row, an
-// MMA warp, a Q slot, two score buffers and an output accumulator in TMEM each), work side by side: on an item's two query
-// tiles, or, when it has one, on alternate key tiles of the same rows; the item's owner (A and B in turn) then joins the
-// two accumulators.
+// the next item's keys run while the current one ends.  Two groups, A and B (128 softmax threads, one per query row, a
+// score and a P V warp, a Q slot, two score buffers and an output accumulator in TMEM each), work side by side: on an
+// item's two query tiles, or, when it has one, on alternate key tiles of the same rows; the item's owner (A and B in turn)
+// then joins the two accumulators.
 //   * warps 0-3 and 4-7: the groups' softmax.  A group's first thread also copies its next item's Q, once the scores of
 //     its last key tile of the current item are there (nothing reads the old Q any more);
-//   * warps 9 and 11: the groups' MMAs (tcgen05), scores one key tile ahead of P V.  One warp for both groups' scores and
-//     one for both groups' P V, tried first, took 1044 cycles per issue (waits, loop and issue in turn), 2090 per key tile
-//     of two query tiles, with the tensor pipe busy for 1300 of them;
+//   * warps 9 and 13: the groups' scores (tcgen05), one key tile ahead of P V, which warps 11 and 15 issue.  One warp for
+//     both groups' scores and one for both groups' P V, tried first, took 1044 cycles per issue (waits, loop and issue in
+//     turn), 2090 per key tile of two query tiles;
 //   * warps 8 and 10: copy the K and V tiles (TMA, one block of the block table per copy, one lane per block);
 //   * INT8 caches: warps 16-19 widen the codes to f16, two warps per operand, half of the rows each.
 // Hand-offs are mbarriers; every wait is bounded.  On a timeout a role records the error and does nothing more, the CTA
 // drains its own MMAs and copies (bounded) and frees TMEM.
+//
+// What bounds it: a key tile of two query tiles takes 1780 cycles (bf16) where its MMAs need 1296 (scores 128 x 64 x 16 from
+// shared memory 48.7 cycles each, P V 128 x 128 x 16 with P in TMEM 64.6).  The rest is the chain of hand-offs through the two
+// score buffers (P over the scores that it was made of): softmax 1370 cycles, P seen by its warp 370, P V 570, the next scores
+// 1030.  Half of the score MMAs, half of the P V MMAs or no exponentials at all take 4 to 6% off, no more.  Tried and slower:
+// P in columns of its own beside one score buffer per group (+11%) or three between the groups (+20%), one arrival per warp
+// instead of one per thread (+3%).
 #include <algorithm>
 
 #include "full_tile.cuh"
@@ -34,12 +43,22 @@ namespace pkv {
 
 namespace {
 
-// Fewest units in a share (even): a piece costs a record and its joining whatever its length.
+// Fewest units in a share (even): a piece costs a record and its joining whatever its length.  128 sequences over 800 INT8
+// tokens took 33 us with 4, 29 with 8, 33 with 16.
 constexpr int kMinShare = 8;
 // What an item costs beside its key tiles, which count w units each (w: query tiles).  4 units for either kind, tried first,
 // left the SMs with many short items of two query tiles behind: 12 prompts over long states took 810 us against 785.
 __device__ constexpr int item_units(int w) { return 4 * w; }
 constexpr int kBatch = 128;    // items that a CTA lists at a time
+constexpr int kEmpty = 512;    // chunks without keys that it lists
+// Cross attention, at least two items for every CTA, and long ones: the items, ordered by KV head, are first handed out whole,
+// one per CTA and round, so that the query tiles of one head run side by side over the same keys; what is left (an item or
+// two per CTA) is cut so that all CTAs end together.  Cut from the start, the stream's places lie anywhere in a head's keys
+// and every query tile reads them from DRAM: 3.9 GB instead of 1.3 for 12 prompts of 1000 tokens over states of 4500
+// (790 us; 717 with rounds), and 2048 rows over 8192 keys in 8 sequences 472 us instead of 430.  With shorter items the
+// keys stay in L2 anyway, and the rounds' plan (4 us) is not worth it.
+constexpr int kRounds = 64;      // most rounds
+constexpr int kRoundUnits = 64;  // fewest units per item, on average
 
 template <int NARROW>
 struct FullPlan {
@@ -52,9 +71,11 @@ struct FullPlan {
     static constexpr int kOffStg = kOffV + kStages * kStage;
     static constexpr int kOffMeta = kOffStg + 2 * kSlots * kStgSlot;
     static constexpr int kThreads = NARROW == 2 ? 640 : 512;
-    // registers per thread after the split: 256 x 184 + 256 x 72 = 512 x 128, what the launch gives;
-    // 256 x 168 + 384 x 48 = 640 x 96
-    static constexpr int kRegsSoftmax = NARROW == 2 ? 168 : 184, kRegsOther = NARROW == 2 ? 48 : 72;
+    // registers per thread after the split: 256 x 176 + 256 x 80 = 256 x 184 + 256 x 72 = 512 x 128, what the launch gives;
+    // 256 x 168 + 384 x 48 = 640 x 96.  bf16 168 / 176 / 184 / 192 / 200 softmax registers: cross_prompts 706 / 703 / 714 /
+    // 701 / 702 us, 256 queries over 32768 keys 206 / 203 / 209 / 207 / 207; FP8: those queries 246 / 252 / 241 / 247 / 250.
+    static constexpr int kRegsSoftmax = NARROW == 2 ? 168 : NARROW == 1 ? 184 : 176;
+    static constexpr int kRegsOther = NARROW == 2 ? 48 : NARROW == 1 ? 72 : 80;
 };
 
 // mbarriers
@@ -73,9 +94,10 @@ constexpr int kFMine = kFPart + 256;                // ints: x0, x1; the lister'
                                                     // the first item's index; + group: the V stage with rows to be zeroed
 constexpr int kFItems = 912;
 constexpr int kFMlOut = kFItems + 32 * kBatch;      // (m, l) of the other group's rows, [owner][128]
-constexpr int kFUnits = kFMlOut + 2 * 128 * 8;      // the chunks' first units, [kMaxSeqs]
-constexpr int kFEnd = kFUnits + 4 * kMaxSeqs;
-static_assert(kFMine + 40 <= kFItems, "meta slots overlap");
+constexpr int kFUnits = kFMlOut + 2 * 128 * 8;      // the chunks' first units, [kMaxSeqs + 1]
+constexpr int kFFirst = kFUnits + 4 * (kMaxSeqs + 1);  // and first items
+constexpr int kFEnd = kFFirst + 4 * (kMaxSeqs + 1);
+static_assert(kFMine + 52 <= kFItems, "meta slots overlap");
 
 // One CTA's part of an item
 struct Item {
@@ -133,9 +155,11 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(meta + kFAbort);
     int* part = reinterpret_cast<int*>(meta + kFPart);
     int* first_unit = reinterpret_cast<int*>(meta + kFUnits);
+    int* first_item = reinterpret_cast<int*>(meta + kFFirst);
     volatile int* mine = reinterpret_cast<volatile int*>(meta + kFMine);
     Item* items = reinterpret_cast<Item*>(meta + kFItems);
     float2* ml_out = reinterpret_cast<float2*>(meta + kFMlOut);
+    int* empty = reinterpret_cast<int*>(ml_out);  // while the plan is made: chunks without keys
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, ncta = gridDim.x;
     const int g_shift = 31 - __clz(a.G);  // G divides 128
@@ -155,6 +179,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     }
     if (tid == 0) {
         *abort_flag = 0;
+        mine[11] = 0;
         prefetch_tensormap(&qmap);
     }
     if (warp == 8 && lane == 0) prefetch_tensormap(&kmap);
@@ -164,6 +189,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         tmem_relinquish();
     }
 
+    __syncthreads();
     // ---- the plan.  A malformed chunk has nothing to do.
     auto load_chunk = [&](int c, bool report) {
         Chunk k;
@@ -181,9 +207,10 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         k.items = k.kt > 0 ? ((k.tokens + cta_q - 1) >> cta_shift) * a.Hkv : 0;
         return k;
     };
-    // Part of item m (KV head and query tiles) of a chunk whose first unit is `start`, into the list.
-    auto put_item = [&](int slot, const Chunk& k, int start, int m, bool first) {
-        const int x0 = mine[0], x1 = mine[1], tile = m / a.Hkv, h = m - tile * a.Hkv, t0 = tile << cta_shift;
+    // What [x0, x1) holds of item m (KV head and query tiles) of a chunk whose first unit is `start`, into the list.
+    auto put_item = [&](int slot, const Chunk& k, int start, int m, int x0, int x1, int rounds, bool first) {
+        const int n_tiles = (k.tokens + cta_q - 1) >> cta_shift;
+        const int tile = rounds ? m % n_tiles : m / a.Hkv, h = rounds ? m / n_tiles : m - tile * a.Hkv, t0 = tile << cta_shift;
         const int Uk = start + m * k.ku, j0 = max(0, x0 - Uk - item_units(k.w)) >> (k.w - 1);
         Item it;
         it.q_row = k.q0 + t0;
@@ -208,6 +235,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         const int c_lo = min(tid * per, n_chunks), c_hi = min(c_lo + per, n_chunks);
         int sum = 0, count = 0, before = 0, items_at = 0, x0 = 0, x1 = 0;  // units and items; of the chunks before this thread's
         Chunk k = {};
+        int rounds = 0;  // of whole items, one per CTA
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             int run = before, index = items_at;
@@ -218,6 +246,10 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 if (pass == 0) {
                     sum = add_units(sum, units);
                     count += k.items;
+                    if (!f.prefix && k.keys == 0 && k.tokens > 0) {
+                        const int e = atomicAdd(const_cast<int*>(mine) + 11, 1);
+                        if (e < kEmpty) empty[e] = c;
+                    }
                 } else if (pass == 1) {
                     first_unit[c] = run;
                     if (run <= x0 && x0 < run + units && x0 < x1) {  // where this CTA starts
@@ -228,10 +260,10 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         mine[7] = index + m;
                     }
                 } else if (x0 < x1 && run + units > x0 && run < x1) {
-                    const int m0 = max(0, mine[7] - index), m1 = items_before(k, run, x1), slot0 = index - mine[7];
+                    const int m0 = max(0, mine[7] - index), m1 = items_before(k, run, x1), slot0 = index - mine[7] + rounds;
                     const int m2 = min(m1, kBatch - slot0);
 #pragma unroll 1
-                    for (int m = m0; m < m2; ++m) put_item(slot0 + m, k, run, m, slot0 + m == 0);
+                    for (int m = m0; m < m2; ++m) put_item(slot0 + m, k, run, m, x0, x1, rounds, slot0 + m == rounds);
                     if (m2 > m0) atomicMax(const_cast<int*>(mine) + 5, slot0 + m2);
                     if (m1 > m2 && m2 >= m0 && slot0 + m0 <= kBatch) {  // the list is full: the next batch starts here
                         mine[2] = c;
@@ -274,7 +306,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             }
             int T = __shfl_sync(kFull, iu, 31);
             const int bu = __shfl_sync(kFull, iu, max(0, warp - 1));
-            const int bc = __shfl_sync(kFull, ic, max(0, warp - 1));
+            const int bc = __shfl_sync(kFull, ic, max(0, warp - 1)), M = __shfl_sync(kFull, ic, 31);
             if (warp) {
                 before += bu;
                 items_at += bc;
@@ -286,15 +318,88 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             } else {
                 share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
             }
-            x0 = static_cast<int>(min(static_cast<int64_t>(cta) * share, static_cast<int64_t>(T)));
-            x1 = static_cast<int>(min(static_cast<int64_t>(x0) + share, static_cast<int64_t>(T)));
+            if (!f.prefix && M >= 2 * ncta && T / M >= kRoundUnits) rounds = min(kRounds, M / ncta - 1);
             if (tid == 0) {
-                mine[0] = x0;
-                mine[1] = x1;
-                mine[5] = mine[6] = 0;
-                if (cta == ncta - 1) *f.share = share;
+                mine[5] = mine[12] = rounds;
+                mine[6] = 0;
                 f.cuts[cta] = make_int4(0, 0, 0, 0);
+                if (cta == ncta - 1) *f.share = rounds ? 0 : share;
             }
+            if (rounds == 0) {
+                x0 = static_cast<int>(min(static_cast<int64_t>(cta) * share, static_cast<int64_t>(T)));
+                x1 = static_cast<int>(min(static_cast<int64_t>(x0) + share, static_cast<int64_t>(T)));
+                if (tid == 0) {
+                    mine[0] = x0;
+                    mine[1] = x1;
+                }
+                continue;
+            }
+            // Rounds: where the rest begins, then what each CTA still takes of it
+            const int rest = rounds * ncta;  // the first item that is in no round
+            int u = before, n = items_at;
+#pragma unroll 1
+            for (int c = c_lo; c < c_hi; ++c) {
+                if (per > 1) k = load_chunk(c, false);
+                first_unit[c] = u;
+                first_item[c] = n;
+                if (n <= rest && rest < n + k.items) mine[10] = u + (rest - n) * k.ku;
+                u += k.items * k.ku;
+                n += k.items;
+            }
+            if (tid == 0) {
+                first_unit[n_chunks] = T;
+                first_item[n_chunks] = M;
+            }
+            __syncthreads();
+            auto chunk_of = [&](int item) {
+                int lo = 0, hi = n_chunks - 1;
+#pragma unroll 1
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (first_item[mid] <= item) lo = mid;
+                    else hi = mid - 1;
+                }
+                return lo;
+            };
+            const int origin = mine[10];
+            int part_c = 0;  // of the rest, for CTA tid
+            if (tid < ncta) {
+                int load = 0;
+#pragma unroll 1
+                for (int r = 0; r < rounds; ++r) {
+                    const int c = chunk_of(r * ncta + tid);
+                    load += (first_unit[c + 1] - first_unit[c]) / (first_item[c + 1] - first_item[c]);
+                }
+                part_c = max(0, share - load);
+            }
+            if (tid < rounds) {
+                const int item = tid * ncta + cta, c = chunk_of(item), m = item - first_item[c];
+                const Chunk w = load_chunk(c, false);
+                const int U = first_unit[c] + m * w.ku;
+                put_item(tid, w, first_unit[c], m, U, U + w.ku, rounds, false);
+            }
+            int upto = part_c;
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (lane == 31) part[warp] = upto;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) upto += part[w];
+            if (tid < ncta) {
+                const int x = min(upto - part_c, T - origin), y = min(upto, T - origin);
+                if (tid == cta) {
+                    mine[0] = x;
+                    mine[1] = y;
+                }
+                if (cta == ncta - 1) f.points[tid] = x;
+                if (cta == ncta - 1 && tid == ncta - 1) f.points[ncta] = T - origin;
+            }
+            __syncthreads();
+            before -= origin;
+            x0 = mine[0];
+            x1 = mine[1];
         }
     }
     const uint32_t tmem = *tmem_slot;
@@ -325,7 +430,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             }
             const int pos = n + ic - cnt, fits = min(cnt, max(0, kBatch - pos)), total = __shfl_sync(kFull, ic, 31);
 #pragma unroll 1
-            for (int i = 0; i < fits; ++i) put_item(pos + i, k, start, k_lo + i, false);
+            for (int i = 0; i < fits; ++i) put_item(pos + i, k, start, k_lo + i, mine[0], x1, mine[12], false);
             if (n + total > kBatch) {  // the first lane whose items do not all fit is where the next batch starts
                 const unsigned over = __ballot_sync(kFull, pos + cnt > kBatch);
                 if (lane == __ffs(over) - 1) {
@@ -364,20 +469,30 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         }
     };
 
-    // ---- what the joining needs to know of each sequence, and the rows without keys: from the last CTA down, the first
-    // have work in any case
+    // ---- what the joining needs to know of each sequence (from the last CTA down, the first have work in any case), or the
+    // rows without keys: each chunk of them by all CTAs.  (One CTA per chunk took 170 us for 1249 tokens of 32 heads.)
+    auto zero_rows = [&](int c, size_t first, size_t stride) {
+        const Chunk k = load_chunk(c, false);
+        uint4* o = reinterpret_cast<uint4*>(a.out) + static_cast<size_t>(k.q0) * a.Hq * 16;
 #pragma unroll 1
-    for (int s = ncta - 1 - cta; s < a.nseq; s += ncta) {
-        const Chunk k = load_chunk(s, false);
-        if (f.prefix) {
+        for (size_t i = first; i < static_cast<size_t>(k.tokens) * a.Hq * 16; i += stride) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    };
+    const int n_empty = mine[11];
+    if (f.prefix) {
+#pragma unroll 1
+        for (int s = ncta - 1 - cta; s < n_chunks; s += ncta) {
+            const Chunk k = load_chunk(s, false);
             for (int i = tid; i < k.tokens; i += kNT)
                 f.seq_plan[k.q0 + i] = make_int4(first_unit[s] + (i >> cta_shift) * a.Hkv * k.ku + item_units(k.w), k.ku, (i & (cta_q - 1)) << g_shift,
                                                   k.ku - item_units(k.w));
-        } else if (k.keys == 0) {
-            uint4* o = reinterpret_cast<uint4*>(a.out) + static_cast<size_t>(k.q0) * a.Hq * 16;
-#pragma unroll 1
-            for (size_t i = tid; i < static_cast<size_t>(k.tokens) * a.Hq * 16; i += kNT) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
+    } else if (n_empty <= kEmpty) {
+#pragma unroll 1
+        for (int e = 0; e < n_empty; ++e) zero_rows(empty[e], static_cast<size_t>(cta) * kNT + tid, static_cast<size_t>(ncta) * kNT);
+    } else {
+#pragma unroll 1
+        for (int s = cta; s < n_chunks; s += ncta)
+            if (load_chunk(s, false).keys == 0) zero_rows(s, tid, kNT);
     }
 
     // the preparing kernel has completed; only then may the next one start, which uses what it cleared
@@ -881,17 +996,24 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const PrefillArgs a, con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 cut = f.cuts[c];
-    const int share = *f.share, U0 = cut.z, U1 = cut.w;
+    const int U0 = cut.z, U1 = cut.w;
     // the item's first extra piece does it: the cut before it, if any, falls before the item or in its first units
-    if (U1 == 0 || (c - 1) * share > U0) return;
-    const int valid = (cut.y & 0xffff) * a.G, h = cut.y >> 16, c_last = (U1 - 1) / share;
+    if (U1 == 0) return;
+    const int share = *f.share;  // 0: the cuts are listed
+    auto point = [&](int k) { return share ? k * share : f.points[k]; };
+    int prev = c - 1;
+    while (prev > 0 && point(prev) == point(c)) --prev;
+    if (prev >= 0 && point(prev) > U0) return;
+    const int valid = (cut.y & 0xffff) * a.G, h = cut.y >> 16, c_end = gridDim.x;
 #pragma unroll 1
     for (int r = blockIdx.y * 32 + warp; r < min(valid, static_cast<int>(blockIdx.y) * 32 + 32); r += 8) {
         const size_t row = (static_cast<size_t>(cut.x) + r / a.G) * a.Hq + static_cast<size_t>(h) * a.G + r % a.G;
         Joined j;
         j.add(f, row, lane);
 #pragma unroll 2
-        for (int k = c; k <= c_last; ++k) j.add(f, static_cast<size_t>(f.extra_row) + static_cast<size_t>(k) * 256 + r, lane);
+        for (int k = c; k < c_end && point(k) < U1; ++k)
+            if (share || f.points[k] < f.points[k + 1])
+                j.add(f, static_cast<size_t>(f.extra_row) + static_cast<size_t>(k) * 256 + r, lane);
         j.store(a, row, h, lane);
     }
 }

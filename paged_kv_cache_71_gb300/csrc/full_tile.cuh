@@ -17,7 +17,8 @@ struct FullArgs {
     float2* rec_ml;      // [rows]
     int64_t extra_row;   // first row of the CTAs': total_q_tokens * Hq
     const float* q_scale;  // one-byte caches: [rows] of (token, query head), what the operands' scores are multiplied by
-    int* share;          // stream units per CTA
+    int* share;          // stream units per CTA; 0: `points`
+    int* points;         // [CTAs + 1] where the CTAs' parts of the stream start, when they differ
     int4* cuts;          // [CTAs] {first token, tokens | head << 16, U0, U1} of the item that the CTA's share starts inside
                          // of, its key tiles at units [U0, U1) of the stream; U1 = 0: none
     int4* seq_plan;      // shared prefixes: [sequences] {first key tile's unit of KV head 0's item, units per item, row in the

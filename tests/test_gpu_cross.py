@@ -126,6 +126,25 @@ def test_items_longer_and_shorter_than_a_share(kv):
     assert int(b.err) == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_several_long_items_for_every_sm(kv):
+    """352 items of 47 to 125 key tiles, one or two query tiles each: whole items in rounds, then a stream of the rest."""
+    b = Batch([300, 40, 129, 5, 260, 500, 128, 257], [3000, 4100, 0, 8000, 4500, 3333, 4096, 5000], 32, 1, 16, kv, seed=9).device()
+    b.run()
+    b.verify(f"{kv} rounds")
+    assert int(b.err) == 0
+
+
+def test_many_sequences_without_states():
+    """More of them than an SM lists, and one of many tokens."""
+    tokens, states = [1, 2] * 300 + [300, 5], [0] * 601 + [70]
+    b = Batch(tokens, states, 2, 4, 16, "bf16", seed=10).device()
+    b.run()
+    torch.cuda.synchronize()
+    assert (b.out[:b.cu[601]] == 0).all() and int(b.err) == 0
+    b.verify("many without states", skip=range(601))
+
+
 @pytest.mark.parametrize("kv", ["fp8", "int8"])
 def test_per_head_scales(kv):
     b = Batch(TOKENS, STATES, 2, 4, 16, kv, seed=3, head_scales=True).device()
