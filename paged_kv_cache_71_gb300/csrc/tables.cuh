@@ -18,6 +18,7 @@ struct ExtendArgs {
     int64_t* slots;              // [max_tokens]
     int32_t* err;                // nullable
     int N, MB, shift, NB, max_tokens;  // shift: log2 of the block size
+    int runs = 1;                      // consecutive slots of a thread (set by the launcher)
 };
 
 struct ReleaseArgs {
