@@ -990,32 +990,28 @@ struct Joined {
 
 }  // namespace
 
-// Block (c, part) takes rows [32 part, 32 part + 32) of the item whose second piece starts CTA c's share;
-// one warp per row.
+// Block (c, part) takes rows [8 part, 8 part + 8) of the item whose second piece starts CTA c's share; one warp per row.
+// (With 32 rows per block, four per warp in turn, 24 x 5 tokens over 1150 FP8 states took 38 us instead of 34.7.)
 __global__ void __launch_bounds__(256) join_cuts_kernel(const PrefillArgs a, const FullArgs f) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, ncta = gridDim.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int4 cut = f.cuts[c];
-    const int U0 = cut.z, U1 = cut.w;
+    const int share = *f.share;  // 0: the parts' starts are listed
+    const int U0 = cut.z, U1 = cut.w, h = cut.y >> 16;
+    if (U1 == 0 || r >= (cut.y & 0xffff) * a.G) return;
+    auto start = [&](int k) { return share ? k * share : f.points[k]; };
     // the item's first extra piece does it: the cut before it, if any, falls before the item or in its first units
-    if (U1 == 0) return;
-    const int share = *f.share;  // 0: the cuts are listed
-    auto point = [&](int k) { return share ? k * share : f.points[k]; };
     int prev = c - 1;
-    while (prev > 0 && point(prev) == point(c)) --prev;
-    if (prev >= 0 && point(prev) > U0) return;
-    const int valid = (cut.y & 0xffff) * a.G, h = cut.y >> 16, c_end = gridDim.x;
-#pragma unroll 1
-    for (int r = blockIdx.y * 32 + warp; r < min(valid, static_cast<int>(blockIdx.y) * 32 + 32); r += 8) {
-        const size_t row = (static_cast<size_t>(cut.x) + r / a.G) * a.Hq + static_cast<size_t>(h) * a.G + r % a.G;
-        Joined j;
-        j.add(f, row, lane);
+    while (prev > 0 && start(prev) == start(c)) --prev;  // (a part may be empty)
+    if (prev >= 0 && start(prev) > U0) return;
+    const size_t row = (static_cast<size_t>(cut.x) + r / a.G) * a.Hq + static_cast<size_t>(h) * a.G + r % a.G;
+    const size_t extra = static_cast<size_t>(f.extra_row) + r;
+    Joined j;
+    j.add(f, row, lane);
 #pragma unroll 2
-        for (int k = c; k < c_end && point(k) < U1; ++k)
-            if (share || f.points[k] < f.points[k + 1])
-                j.add(f, static_cast<size_t>(f.extra_row) + static_cast<size_t>(k) * 256 + r, lane);
-        j.store(a, row, h, lane);
-    }
+    for (int k = c; k < ncta && start(k) < U1; ++k)
+        if (share || f.points[k] < f.points[k + 1]) j.add(f, extra + static_cast<size_t>(k) * 256, lane);
+    j.store(a, row, h, lane);
 }
 
 // Shared prefixes: one warp per (sequence, query head).
@@ -1147,7 +1143,7 @@ static cudaError_t launch_beside(Kernel kern, dim3 grid, const PrefillArgs& a, c
 }
 
 cudaError_t launch_join_cuts(const PrefillArgs& a, const FullArgs& f, int grid, cudaStream_t stream) {
-    return launch_beside(join_cuts_kernel, dim3(grid, 8), a, f, stream);
+    return launch_beside(join_cuts_kernel, dim3(grid, 32), a, f, stream);
 }
 
 cudaError_t launch_join_rows(const PrefillArgs& a, const FullArgs& f, cudaStream_t stream) {
