@@ -156,6 +156,10 @@ def test_more_items_than_a_block_lists_at_a_time():
     _check(Batch([(16, [1, i % 3]) for i in range(160)], 128, 1, 16, "bf16", seed=16), "many items", range(0, 320, 23))
 
 
+def test_groups_without_sequences():
+    _check(Batch([(48, []), (64, [1, 20]), (32, []), (0, []), (160, [33])], 2, 4, 16, "bf16", seed=17), "empty groups")
+
+
 def test_single_sequence_and_no_prefix_at_all():
     _check(Batch([(0, [1])], 8, 4, 16, "bf16", seed=6), "one token")
     _check(Batch([(16, [0])], 8, 4, 16, "bf16", seed=6), "one block, no own tokens")
