@@ -1299,6 +1299,8 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
         return fail(PKV_ERR_UNSUPPORTED, "num_groups %d > %d groups per call", num_groups, prefill_ws_max_seqs());
     if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq * Hkv > INT32_MAX - 64)
         return fail(PKV_ERR_OUT_OF_RANGE, "num_seqs * max_blocks_per_seq * num_kv_heads must stay below 2^31");
+    if (static_cast<int64_t>(max_blocks_per_seq) * S > INT32_MAX - 64)
+        return fail(PKV_ERR_OUT_OF_RANGE, "a row of the block table holds more than 2^31-65 tokens");
     if (!(scale > 0.f && scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and positive");
     if (num_seqs == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_groups || !prefix_lens)

@@ -74,6 +74,7 @@ def test_prefix_decode_host_checks():
     assert _prefix(ng=2049) == 2
     assert _prefix(ng=0) == 1                         # every sequence belongs to a group
     assert _prefix(n=8192, mb=1 << 16) == 3
+    assert _prefix(desc=_desc(num_kv_heads=1), Hq=8, n=1, mb=1 << 28) == 3
     assert _prefix(scale=0.0) == 1
     assert _prefix(scale=float("nan")) == 1
     assert _prefix(scale=-1.0) == 1
