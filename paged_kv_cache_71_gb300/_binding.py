@@ -263,11 +263,21 @@ def _device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
+def _here(t) -> int:
+    """The current CUDA device, which t must be on (-2: it is on none, and CUDA may not have been used)."""
+    return torch._C._cuda_getDevice() if t.get_device() >= 0 else -2
+
+
+def _extra(t, device: int) -> bool:
+    """A workspace or error word: a tensor must be on the device; None and raw pointers pass."""
+    return t is None or isinstance(t, int) or t.get_device() == device
+
+
 def _fits(t, dtype, shape, device: int) -> bool:
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device
 
 
-def _refuse(func: str, device: int, **tensors) -> None:
+def _refuse(func: str, device: int, device_error=None, workspace=None, **tensors) -> None:
     """Say what is wrong with tensors that the pointers alone would not tell from good ones: name=(tensor or None, dtypes,
     shape).  Layouts must be contiguous, and every tensor on the current CUDA device."""
     tensors = {name: x for name, x in tensors.items() if x[0] is not None}
@@ -281,6 +291,9 @@ def _refuse(func: str, device: int, **tensors) -> None:
     for name, (t, _, _) in tensors.items():
         if t.get_device() != device:
             raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
+    for name, t in (("device_error", device_error), ("workspace", workspace)):
+        if not _extra(t, device):
+            raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
 
 
 _I32, _I64, _FLAG = (torch.int32,), (torch.int64,), (torch.bool, torch.uint8)
@@ -292,19 +305,19 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
                          stream=None) -> None:
     """Block tables, lengths and slot map of a step from the request lengths, on the GPU.  seq_lens may be past_lens and
     new_free_count may be free_count (in place); free_blocks has one entry per block of the pool."""
-    L, (n,), i32 = lib(), past_lens.shape, torch.int32
-    width, nb, cap, dev = block_tables.shape[-1], free_blocks.numel(), slot_mapping.numel(), _device()
+    L, shape, rows, i32, dev = lib(), past_lens.shape, block_tables.shape, torch.int32, _here(past_lens)
+    (n,), width, nb, cap = shape, rows[-1], free_blocks.numel(), slot_mapping.numel()
     if not (block_tables.dtype is past_lens.dtype is new_lens.dtype is free_blocks.dtype is free_count.dtype
             is seq_lens.dtype is new_free_count.dtype is i32 and slot_mapping.dtype is torch.int64
-            and block_tables.shape == (n, width) and new_lens.shape == seq_lens.shape == past_lens.shape
-            and free_count.shape == new_free_count.shape == (1,) and free_blocks.dim() == slot_mapping.dim() == 1
+            and rows == (n, width) and new_lens.shape == shape == seq_lens.shape
+            and free_count.numel() == new_free_count.numel() == free_blocks.dim() == slot_mapping.dim() == 1
             and block_tables.is_contiguous() and past_lens.is_contiguous() and new_lens.is_contiguous()
             and free_blocks.is_contiguous() and seq_lens.is_contiguous() and slot_mapping.is_contiguous()
             and block_tables.get_device() == past_lens.get_device() == new_lens.get_device() == free_blocks.get_device()
             == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device()
-            == slot_mapping.get_device() == dev
-            and (cu_q is None or _fits(cu_q, i32, (n + 1,), dev)) and (q_starts is None or _fits(q_starts, i32, (n,), dev))):
-        _refuse("pkv_extend_sequences", dev, block_tables=(block_tables, _I32, (n, width)), past_lens=(past_lens, _I32, (n,)),
+            == slot_mapping.get_device() == dev and _extra(device_error, dev)
+            and (cu_q is None or _fits(cu_q, i32, (n + 1,), dev)) and (q_starts is None or _fits(q_starts, i32, shape, dev))):
+        _refuse("pkv_extend_sequences", _device(), device_error, block_tables=(block_tables, _I32, (n, width)), past_lens=(past_lens, _I32, (n,)),
                 new_lens=(new_lens, _I32, (n,)), free_blocks=(free_blocks, _I32, (nb,)), free_count=(free_count, _I32, (1,)),
                 seq_lens=(seq_lens, _I32, (n,)), new_free_count=(new_free_count, _I32, (1,)),
                 slot_mapping=(slot_mapping, _I64, (cap,)), cu_q=(cu_q, _I32, (n + 1,)), q_starts=(q_starts, _I32, (n,)))
@@ -319,18 +332,18 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
 def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, free_blocks, free_count, seq_lens,
                           new_free_count, keep_blocks=None, device_error=None, stream=None) -> None:
     """Finished sequences hand their blocks back to the free stack, on the GPU (finished: bool or uint8 [num_seqs])."""
-    L, (n,), i32 = lib(), past_lens.shape, torch.int32
-    width, nb, dev = block_tables.shape[-1], free_blocks.numel(), _device()
+    L, shape, rows, i32, dev = lib(), past_lens.shape, block_tables.shape, torch.int32, _here(past_lens)
+    (n,), width, nb = shape, rows[-1], free_blocks.numel()
     if not (block_tables.dtype is past_lens.dtype is free_blocks.dtype is free_count.dtype is seq_lens.dtype
             is new_free_count.dtype is i32 and finished.dtype in _FLAG
-            and block_tables.shape == (n, width) and finished.shape == seq_lens.shape == past_lens.shape
-            and free_count.shape == new_free_count.shape == (1,) and free_blocks.dim() == 1
+            and rows == (n, width) and finished.shape == shape == seq_lens.shape
+            and free_count.numel() == new_free_count.numel() == free_blocks.dim() == 1
             and block_tables.is_contiguous() and past_lens.is_contiguous() and finished.is_contiguous()
             and free_blocks.is_contiguous() and seq_lens.is_contiguous()
             and block_tables.get_device() == past_lens.get_device() == finished.get_device() == free_blocks.get_device()
             == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device() == dev
-            and (keep_blocks is None or _fits(keep_blocks, i32, (n,), dev))):
-        _refuse("pkv_release_sequences", dev, block_tables=(block_tables, _I32, (n, width)),
+            and _extra(device_error, dev) and (keep_blocks is None or _fits(keep_blocks, i32, shape, dev))):
+        _refuse("pkv_release_sequences", _device(), device_error, block_tables=(block_tables, _I32, (n, width)),
                 past_lens=(past_lens, _I32, (n,)), finished=(finished, _FLAG, (n,)), free_blocks=(free_blocks, _I32, (nb,)),
                 free_count=(free_count, _I32, (1,)), seq_lens=(seq_lens, _I32, (n,)),
                 new_free_count=(new_free_count, _I32, (1,)), keep_blocks=(keep_blocks, _I32, (n,)))
@@ -355,15 +368,16 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
                                       stream=None) -> None:
     """Decode attention for groups of sequences (cu_groups) that share their first prefix_lens tokens' blocks: a group's
     prefix is computed once for all of its sequences."""
-    L, (n, heads, D), dev = lib(), q.shape, _device()
+    L, (n, heads, D), dev = lib(), q.shape, _here(q)
     caches, groups, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), prefix_lens.numel(), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES
+    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES and _extra(workspace, dev)
+            and _extra(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
             and _fits(block_tables, torch.int32, (n, width), dev) and _fits(context_lens, torch.int32, (n,), dev)
             and _fits(cu_groups, torch.int32, (groups + 1,), dev) and _fits(prefix_lens, torch.int32, (groups,), dev)):
         caches = (*caches[:3], cache.head_dim)
-        _refuse("pkv_paged_attention_decode_prefix", dev, q=(q, _FLOATS, (n, heads, cache.head_dim)),
+        _refuse("pkv_paged_attention_decode_prefix", _device(), device_error, workspace, q=(q, _FLOATS, (n, heads, cache.head_dim)),
                 out=(out, (q.dtype,), (n, heads, D)), k_cache=(k_cache, _CACHES, caches),
                 v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
                 context_lens=(context_lens, _I32, (n,)), cu_groups=(cu_groups, _I32, (groups + 1,)),
@@ -391,15 +405,16 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
                               workspace=None, device_error=None, stream=None) -> None:
     """Decoder queries against paged encoder states, without a mask: sequence s owns query tokens
     [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
-    L, (tokens, heads, D), n, dev = lib(), q.shape, kv_lens.numel(), _device()
+    L, (tokens, heads, D), n, dev = lib(), q.shape, kv_lens.numel(), _here(q)
     caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES
+    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES and _extra(workspace, dev)
+            and _extra(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
             and _fits(block_tables, torch.int32, (n, width), dev) and _fits(kv_lens, torch.int32, (n,), dev)
             and (cu_q is None or _fits(cu_q, torch.int32, (n + 1,), dev))):
         caches = (*caches[:3], cache.head_dim)
-        _refuse("pkv_paged_cross_attention", dev, q=(q, _FLOATS, (tokens, heads, cache.head_dim)),
+        _refuse("pkv_paged_cross_attention", _device(), device_error, workspace, q=(q, _FLOATS, (tokens, heads, cache.head_dim)),
                 out=(out, (q.dtype,), (tokens, heads, D)), kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _CACHES, caches),
                 v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
                 cu_q=(cu_q, _I32, (n + 1,)))

@@ -243,3 +243,15 @@ def test_a_bad_block_is_reported():
     b.run()
     b.verify("the other sequence", skip=[0])
     assert int(b.err) & B.DEVERR_BAD_BLOCK
+
+
+def test_a_workspace_or_error_word_in_host_memory_is_refused():
+    b = Batch([5, 6], [30, 40], 2, 4, 16, "bf16", seed=11).device()
+    for name in ("ws", "err"):
+        kept = getattr(b, name)
+        setattr(b, name, kept.cpu())
+        with pytest.raises(pkv.PkvError, match="workspace" if name == "ws" else "device_error"):
+            b.run()
+        setattr(b, name, kept)
+    b.run()
+    b.verify("after the refusals")

@@ -219,3 +219,11 @@ def test_prefix_groups_keep_the_larger_saving():
     tabs.fork("x", "y")
     cu, pre = tabs.prefix_groups(["x", "y", "root", "z"])    # 5 blocks, 5 blocks, then 4 of all three and of all four
     assert cu.tolist() == [0, 4] and pre.tolist() == [16]
+
+
+def test_workspaces_and_error_words_must_be_where_the_tensors_are():
+    assert B._extra(None, 0) and B._extra(4096, 0) and B._extra(_z(1), -1)
+    assert not B._extra(_z(1), 0) and not B._extra(_z(1), -2)
+    for name, kw in (("device_error", dict(device_error=_z(1))), ("workspace", dict(workspace=_z(16)))):
+        with pytest.raises(pkv.PkvError, match=name):
+            B._refuse("call", 0, **kw)
