@@ -255,3 +255,18 @@ def test_a_workspace_or_error_word_in_host_memory_is_refused():
         setattr(b, name, kept)
     b.run()
     b.verify("after the refusals")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_a_workspace_aligned_to_16_bytes_only(kv):
+    """Exactly as many bytes as asked for, at 16 bytes past a 512-byte boundary; what lies around stays as it is."""
+    b = Batch([3, 200], [9999, 300], 2, 4, 16, kv, seed=12).device()
+    call, verify = b.run, lambda: b.verify(f"{kv} workspace at an odd 16 bytes")
+    need = b.ws.numel()
+    room = torch.full((need + 1024,), 0xab, dtype=torch.uint8, device="cuda")
+    at = -room.data_ptr() % 512 + 16
+    b.ws = room[at:at + need]
+    call()
+    torch.cuda.synchronize()
+    verify()
+    assert (room[:at] == 0xab).all() and (room[at + need:] == 0xab).all()

@@ -296,3 +296,25 @@ def test_groups_that_overlap_beyond_what_can_be_counted_are_reported():
     err = torch.zeros(1, **i32)
     pkv.pkv_paged_attention_decode_prefix(out, q, k, k, desc, tables, lens, cu, pre, 0.1, ws, err)
     assert int(err) & B.DEVERR_BAD_LENGTH
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_a_workspace_aligned_to_16_bytes_only(kv):
+    """Exactly as many bytes as asked for, at 16 bytes past a 512-byte boundary; what lies around stays as it is."""
+    b = Batch(RAGGED, 2, 4, 16, kv, seed=18).device()
+    call, verify = b.run, lambda: check(b.out, *b.reference(), f"{kv} workspace at an odd 16 bytes")
+    need = b.ws.numel()
+    room = torch.full((need + 1024,), 0xab, dtype=torch.uint8, device="cuda")
+    at = -room.data_ptr() % 512 + 16
+    b.ws = room[at:at + need]
+    call()
+    torch.cuda.synchronize()
+    verify()
+    assert (room[:at] == 0xab).all() and (room[at + need:] == 0xab).all()
+
+
+@pytest.mark.parametrize("kv,S,G", [("bf16", 16, 1), ("int8", 32, 1), ("bf16", 32, 8), ("fp8", 8, 2)])
+def test_the_largest_batch(kv, S, G):
+    """8192 sequences in three groups, one of them without a prefix."""
+    b = Batch([(64, [1 + i % 3 for i in range(5000)]), (0, [i % 40 for i in range(3000)]), (32, [2] * 192)], 2, G, S, kv, seed=19)
+    _check(b, f"{kv} S={S} G={G}", [*range(0, 8192, 431), 4999, 5000, 5001, 7999, 8000, 8191])
