@@ -130,6 +130,8 @@ pkv_status pkv_paged_attention_workspace_size(const pkv_cache_desc* cache, int32
  * Chunked Prefill" §2.2 (running max m, running sum l, unnormalised O,
  * rescaled by exp(m_old - m_new) when the max grows; out = O / l).
  * A sequence with context length 0 gets an all-zero row.
+ * (Here and in the other attention calls: a key whose score is -inf has weight
+ * 0, and a row all of whose scores are -inf is zero.)
  *
  * Split-KV: the work of all (sequence, KV head) pairs is laid end to end
  * block by block and cut into equal shares, one per worker warp, so that

@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(32 * DecodePolicy<G, D>::warps, 1)
         const int seg_x0 = A0 + k;
         float2 q2[G][HP];
         float2 o2[G][HP];
-        float m_ref = -INFINITY;  // running max of head gl (log2 units), uniform over lanes holding gl
+        float m_ref = kLowest;    // running max of head gl (log2 units), uniform over lanes holding gl
         float l_run = 0.f;        // this lane's share of the running sum of head gl
         int ma = 0, mc = 0, seg_first = 0;
         bool first = true;

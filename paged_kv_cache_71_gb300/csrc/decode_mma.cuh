@@ -783,7 +783,7 @@ __device__ __forceinline__ void decode_mma_body(const CUtensorMap& kmap, const C
                 for (int hh = 0; hh < HP; ++hh) {
                     const int hk = (ma & 1023) * HP + hh;  // the KV head
                     qm[hh] = a.k_head ? a.q_base * __ldg(a.k_head + hk) : a.q_mul;
-                    m_ref[hh] = -INFINITY;
+                    m_ref[hh] = kLowest;
                     l_run[hh] = 0.f;
                     const uint4* qrow = reinterpret_cast<const uint4*>(
                         reinterpret_cast<const uint8_t*>(a.q) +

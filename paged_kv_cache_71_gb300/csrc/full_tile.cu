@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 const int h = it.head_pair & 0xffff;
                 const size_t tok_row = (static_cast<size_t>(it.q_row) + (row >> g_shift)) * a.Hq + (static_cast<size_t>(h) << g_shift) +
                                        (row & (a.G - 1));
-                float m_ref = -INFINITY, l_run = 0.f;
+                float m_ref = kLowest, l_run = 0.f;
                 // what the scores are multiplied by (log2 units)
                 float sm_log2 = a.k_head ? a.sm_base * __ldg(a.k_head + h) : a.sm_log2;
                 if (NARROW != 0 && valid) {

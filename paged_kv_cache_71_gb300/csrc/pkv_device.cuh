@@ -16,6 +16,10 @@ namespace pkv {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// Where a softmax's running maximum starts: the lowest finite value.  Scores of -inf (keys that hold infinities) then have
+// weight 2^(-inf - m) = 0 however many come first; from -inf the difference of two infinities would be no number.
+constexpr float kLowest = -3.40282347e+38f;
+
 // ------------------------------------------------------------------ errors
 
 __device__ __forceinline__ void raise_error(int32_t* err, int32_t bits) {

@@ -596,7 +596,7 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
         const int qpos = q_start + qi;
         const uint32_t trow = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tO = tmem + kColO + 128 * t + trow;
-        float m_ref = -INFINITY, l_run = 0.f;
+        float m_ref = kLowest, l_run = 0.f;
         int done = 0;
         const bool active = t == 0 || has_b;
         // score scale (log2 units) and output factor of this KV head: per-head scales when given
