@@ -781,6 +781,9 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     if (s < 0.f) raise_error(a.err, PKV_DEVERR_Q_RANGE);
                     sm_log2 *= fabsf(s);
                 }
+                // (a factor below what fp32 holds, of a row of zeros under a small key scale say: as good as none, but the
+                // keys past the last are -inf, and -inf times zero is no number)
+                if (sm_log2 == 0.f) sm_log2 = 1.17549435e-38f;
                 int left = it.keys - (it.j0 + j_first) * kKeys;  // keys from the current tile on
 #pragma unroll 1
                 for (int j = j_first; j < tiles; j += step, left -= step * kKeys, ++c) {
