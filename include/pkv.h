@@ -472,7 +472,8 @@ pkv_status pkv_release_sequences(const int32_t* block_tables, int32_t max_blocks
  *   prefix_lens: [num_groups] device int32: tokens shared by the whole group, a
  *                multiple of block_size (only full blocks are shared), 0 for none,
  *                and no more than the context length of any of its sequences but
- *                those of length 0 (finished, padding), whose rows are zero.
+ *                those of length 0 (finished, padding), whose rows are zero whatever
+ *                their q holds.
  * The prefix is read through the table row of the group's first sequence, of
  * whatever length that is; the other rows' first prefix_lens / block_size entries
  * are not read.

@@ -778,7 +778,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 float sm_log2 = a.k_head ? a.sm_base * __ldg(a.k_head + h) : a.sm_log2;
                 if (NARROW != 0 && valid) {
                     const float s = f.q_scale[tok_row];  // negative: values that the operands cannot carry
-                    if (s < 0.f) raise_error(a.err, PKV_DEVERR_Q_RANGE);
+                    // (not of a sequence of length 0 in a group with a prefix, whose q nobody need have written)
+                    if (s < 0.f && (!f.prefix || f.lens[it.q_row + (row >> g_shift)] > 0)) raise_error(a.err, PKV_DEVERR_Q_RANGE);
                     sm_log2 *= fabsf(s);
                 }
                 // (a factor below what fp32 holds, of a row of zeros under a small key scale say: as good as none, but the
