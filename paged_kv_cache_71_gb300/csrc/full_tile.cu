@@ -118,7 +118,9 @@ struct Chunk {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Sums of units stop at INT_MAX, which only query ranges that overlap (malformed) can reach: the host bounds the others.
+// Most units of a stream.  Only query ranges that overlap (malformed) can have more, the host bounds the others; the room up
+// to INT_MAX, where sums of units stop, is for what is added to a total (the CTAs, an item's length).
+constexpr int kMostUnits = 0x7fffffff - 4096;
 __device__ __forceinline__ int add_units(int a, int b) {
     return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
 }
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 items_at += bc;
             }
             int share = 0x7fffffff;
-            if (T == 0x7fffffff) {  // nothing is done
+            if (T > kMostUnits) {  // nothing is done
                 T = 0;
                 if (cta == 0 && tid == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
             } else {
