@@ -297,7 +297,12 @@ def _refuse(func: str, device: int, device_error=None, workspace=None, **tensors
 
 
 _I32, _I64, _FLAG = (torch.int32,), (torch.int64,), (torch.bool, torch.uint8)
-_FLOATS, _CACHES = (torch.float32, torch.bfloat16), tuple(_DTYPE_CODE)
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _cache_dtypes(cache: CacheDesc) -> tuple:
+    """The tensor types that a cache of the descriptor's type may have."""
+    return tuple(t for t, code in _DTYPE_CODE.items() if code == cache.dtype)
 
 
 def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, free_blocks, free_count, seq_lens,
@@ -370,7 +375,7 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
     prefix is computed once for all of its sequences."""
     L, (n, heads, D), dev = lib(), q.shape, _here(q)
     caches, groups, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), prefix_lens.numel(), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES and _extra(workspace, dev)
+    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _extra(workspace, dev)
             and _extra(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
@@ -378,7 +383,7 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
             and _fits(cu_groups, torch.int32, (groups + 1,), dev) and _fits(prefix_lens, torch.int32, (groups,), dev)):
         caches = (*caches[:3], cache.head_dim)
         _refuse("pkv_paged_attention_decode_prefix", _device(), device_error, workspace, q=(q, _FLOATS, (n, heads, cache.head_dim)),
-                out=(out, (q.dtype,), (n, heads, D)), k_cache=(k_cache, _CACHES, caches),
+                out=(out, (q.dtype,), (n, heads, D)), k_cache=(k_cache, _cache_dtypes(cache), caches),
                 v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
                 context_lens=(context_lens, _I32, (n,)), cu_groups=(cu_groups, _I32, (groups + 1,)),
                 prefix_lens=(prefix_lens, _I32, (groups,)))
@@ -407,7 +412,7 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
     [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
     L, (tokens, heads, D), n, dev = lib(), q.shape, kv_lens.numel(), _here(q)
     caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and k_cache.dtype in _CACHES and _extra(workspace, dev)
+    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _extra(workspace, dev)
             and _extra(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
@@ -415,7 +420,7 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
             and (cu_q is None or _fits(cu_q, torch.int32, (n + 1,), dev))):
         caches = (*caches[:3], cache.head_dim)
         _refuse("pkv_paged_cross_attention", _device(), device_error, workspace, q=(q, _FLOATS, (tokens, heads, cache.head_dim)),
-                out=(out, (q.dtype,), (tokens, heads, D)), kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _CACHES, caches),
+                out=(out, (q.dtype,), (tokens, heads, D)), kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _cache_dtypes(cache), caches),
                 v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
                 cu_q=(cu_q, _I32, (n + 1,)))
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
