@@ -273,6 +273,23 @@ def _extra(t, device: int) -> bool:
     return t is None or isinstance(t, int) or t.get_device() == device
 
 
+def _word(t, device: int) -> bool:
+    """An error word: None, a raw pointer, or a tensor on the device whose elements have room for it."""
+    return t is None or isinstance(t, int) or (t.element_size() >= 4 and t.get_device() == device)
+
+
+def _room(t, device: int) -> bool:
+    """A workspace: None, or a contiguous tensor on the device (a raw pointer has no size)."""
+    return t is None or (not isinstance(t, int) and t.get_device() == device and t.is_contiguous())
+
+
+def _dims(func: str, **tensors) -> None:
+    """name=(tensor, its number of dimensions), for the shapes that sizes are taken from."""
+    for name, (t, n) in tensors.items():
+        if t.dim() != n:
+            raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected {n} dimension{'s' if n > 1 else ''}")
+
+
 def _fits(t, dtype, shape, device: int) -> bool:
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device
 
@@ -291,9 +308,15 @@ def _refuse(func: str, device: int, device_error=None, workspace=None, **tensors
     for name, (t, _, _) in tensors.items():
         if t.get_device() != device:
             raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
+    if isinstance(workspace, int):
+        raise PkvError(4, func, "workspace must be a tensor: a raw pointer has no size")
     for name, t in (("device_error", device_error), ("workspace", workspace)):
         if not _extra(t, device):
             raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
+    if not _word(device_error, device):
+        raise PkvError(1, func, f"device_error has dtype {device_error.dtype}, expected torch.int32")
+    if not _room(workspace, device):
+        raise PkvError(4, func, "workspace must be contiguous")
 
 
 _I32, _I64, _FLAG = (torch.int32,), (torch.int64,), (torch.bool, torch.uint8)
@@ -311,6 +334,8 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
     """Block tables, lengths and slot map of a step from the request lengths, on the GPU.  seq_lens may be past_lens and
     new_free_count may be free_count (in place); free_blocks has one entry per block of the pool."""
     L, shape, rows, i32, dev = lib(), past_lens.shape, block_tables.shape, torch.int32, _here(past_lens)
+    if len(shape) != 1 or len(rows) != 2:
+        _dims("pkv_extend_sequences", past_lens=(past_lens, 1), block_tables=(block_tables, 2))
     (n,), width, nb, cap = shape, rows[-1], free_blocks.numel(), slot_mapping.numel()
     if not (block_tables.dtype is past_lens.dtype is new_lens.dtype is free_blocks.dtype is free_count.dtype
             is seq_lens.dtype is new_free_count.dtype is i32 and slot_mapping.dtype is torch.int64
@@ -320,7 +345,7 @@ def pkv_extend_sequences(block_tables, past_lens, new_lens, block_size: int, fre
             and free_blocks.is_contiguous() and seq_lens.is_contiguous() and slot_mapping.is_contiguous()
             and block_tables.get_device() == past_lens.get_device() == new_lens.get_device() == free_blocks.get_device()
             == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device()
-            == slot_mapping.get_device() == dev and _extra(device_error, dev)
+            == slot_mapping.get_device() == dev and _word(device_error, dev)
             and (cu_q is None or _fits(cu_q, i32, (n + 1,), dev)) and (q_starts is None or _fits(q_starts, i32, shape, dev))):
         _refuse("pkv_extend_sequences", _device(), device_error, block_tables=(block_tables, _I32, (n, width)), past_lens=(past_lens, _I32, (n,)),
                 new_lens=(new_lens, _I32, (n,)), free_blocks=(free_blocks, _I32, (nb,)), free_count=(free_count, _I32, (1,)),
@@ -338,6 +363,8 @@ def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, fr
                           new_free_count, keep_blocks=None, device_error=None, stream=None) -> None:
     """Finished sequences hand their blocks back to the free stack, on the GPU (finished: bool or uint8 [num_seqs])."""
     L, shape, rows, i32, dev = lib(), past_lens.shape, block_tables.shape, torch.int32, _here(past_lens)
+    if len(shape) != 1 or len(rows) != 2:
+        _dims("pkv_release_sequences", past_lens=(past_lens, 1), block_tables=(block_tables, 2))
     (n,), width, nb = shape, rows[-1], free_blocks.numel()
     if not (block_tables.dtype is past_lens.dtype is free_blocks.dtype is free_count.dtype is seq_lens.dtype
             is new_free_count.dtype is i32 and finished.dtype in _FLAG
@@ -347,7 +374,7 @@ def pkv_release_sequences(block_tables, past_lens, finished, block_size: int, fr
             and free_blocks.is_contiguous() and seq_lens.is_contiguous()
             and block_tables.get_device() == past_lens.get_device() == finished.get_device() == free_blocks.get_device()
             == free_count.get_device() == seq_lens.get_device() == new_free_count.get_device() == dev
-            and _extra(device_error, dev) and (keep_blocks is None or _fits(keep_blocks, i32, shape, dev))):
+            and _word(device_error, dev) and (keep_blocks is None or _fits(keep_blocks, i32, shape, dev))):
         _refuse("pkv_release_sequences", _device(), device_error, block_tables=(block_tables, _I32, (n, width)),
                 past_lens=(past_lens, _I32, (n,)), finished=(finished, _FLAG, (n,)), free_blocks=(free_blocks, _I32, (nb,)),
                 free_count=(free_count, _I32, (1,)), seq_lens=(seq_lens, _I32, (n,)),
@@ -373,10 +400,13 @@ def pkv_paged_attention_decode_prefix(out, q, k_cache, v_cache, cache: CacheDesc
                                       stream=None) -> None:
     """Decode attention for groups of sequences (cu_groups) that share their first prefix_lens tokens' blocks: a group's
     prefix is computed once for all of its sequences."""
-    L, (n, heads, D), dev = lib(), q.shape, _here(q)
+    L, dev = lib(), _here(q)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        _dims("pkv_paged_attention_decode_prefix", q=(q, 3), block_tables=(block_tables, 2))
+    n, heads, D = q.shape
     caches, groups, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), prefix_lens.numel(), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _extra(workspace, dev)
-            and _extra(device_error, dev)
+    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _room(workspace, dev)
+            and _word(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
             and _fits(block_tables, torch.int32, (n, width), dev) and _fits(context_lens, torch.int32, (n,), dev)
@@ -410,10 +440,13 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
                               workspace=None, device_error=None, stream=None) -> None:
     """Decoder queries against paged encoder states, without a mask: sequence s owns query tokens
     [cu_q[s], cu_q[s + 1]) of q (cu_q None: one token a sequence) and kv_lens[s] states."""
-    L, (tokens, heads, D), n, dev = lib(), q.shape, kv_lens.numel(), _here(q)
+    L, n, dev = lib(), kv_lens.numel(), _here(q)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        _dims("pkv_paged_cross_attention", q=(q, 3), block_tables=(block_tables, 2))
+    tokens, heads, D = q.shape
     caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
-    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _extra(workspace, dev)
-            and _extra(device_error, dev)
+    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _room(workspace, dev)
+            and _word(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
             and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
             and _fits(block_tables, torch.int32, (n, width), dev) and _fits(kv_lens, torch.int32, (n,), dev)
