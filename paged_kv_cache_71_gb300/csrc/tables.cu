@@ -299,13 +299,20 @@ Shape shape_of(int N, int64_t items, int sms) {
             N <= 256 && items <= 1024 ? 256 : 1024};
 }
 
+// Dynamic shared memory that every kernel may have without being allowed more: 48 KB less the static part (256 bytes, the
+// scan's), rounded down.
+constexpr size_t kFreeSmem = 47 * 1024;
+
 // The kernel, and behind it the state kernel when the state is updated in place and there is more than one CTA to read it.
+// `most`: dynamic shared memory of the largest batch.  A limit is always raised to that, so that no call lowers it between
+// another host thread's raising and launching.
 template <class Kernel, class State, class Args>
-cudaError_t launch(Kernel kern, State state, const Args& a, bool in_place, Shape shape, size_t smem, cudaStream_t stream) {
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t launch(Kernel kern, State state, const Args& a, bool in_place, Shape shape, size_t smem, size_t most,
+                   cudaStream_t stream) {
+    if (smem > kFreeSmem) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
         if (e != cudaSuccess) return e;
     }
     const bool second = in_place && shape.grid > 1;
@@ -327,22 +334,24 @@ cudaError_t launch(Kernel kern, State state, const Args& a, bool in_place, Shape
 
 }  // namespace
 
+static size_t extend_smem(int N) { return (3 * static_cast<size_t>(N) + 2) * 4; }
+static size_t release_smem(int N) { return (2 * static_cast<size_t>(N) + 1) * 4; }
+
 cudaError_t launch_extend_sequences(const ExtendArgs& a, int sms, cudaStream_t stream) {
-    const size_t smem = (3 * static_cast<size_t>(a.N) + 2) * 4;
     const bool in_place = a.seq_lens == a.past_lens || a.new_free_count == a.free_count;
     const Shape shape = shape_of(a.N, a.max_tokens, sms);
     ExtendArgs b = a;
     const int64_t threads = static_cast<int64_t>(shape.grid) * shape.block;
     // (a small step's slots are half padding, which would leave half of one CTA's warps idle: 256 slots 4.6 instead of 3.7 us)
     b.runs = shape.grid == 1 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min(kRuns, (a.max_tokens + threads - 1) / threads)));
-    return launch(extend_sequences_kernel, extend_state_kernel, b, in_place, shape, smem, stream);
+    return launch(extend_sequences_kernel, extend_state_kernel, b, in_place, shape, extend_smem(a.N),
+                  extend_smem(kMaxTableSeqs), stream);
 }
 
 cudaError_t launch_release_sequences(const ReleaseArgs& a, int sms, cudaStream_t stream) {
-    const size_t smem = (2 * static_cast<size_t>(a.N) + 1) * 4;
     const bool in_place = a.seq_lens == a.past_lens || a.new_free_count == a.free_count;
     return launch(release_sequences_kernel, release_state_kernel, a, in_place,
-                  shape_of(a.N, static_cast<int64_t>(a.N) * a.MB, sms), smem, stream);
+                  shape_of(a.N, static_cast<int64_t>(a.N) * a.MB, sms), release_smem(a.N), release_smem(kMaxTableSeqs), stream);
 }
 
 }  // namespace pkv
