@@ -640,21 +640,21 @@ static pkv_status decode_entry(void* out, const void* q, int32_t q_dtype, const 
     if (uses_tensor_core(cache->dtype, G, D, shared))
         return decode_tensor_core(a, *cache, G, num_seqs, k_cache, v_cache, di, shared,
                                   static_cast<cudaStream_t>(stream));
-    const size_t budget = static_cast<size_t>(di.smem_optin) - 256;  // static shared memory of the kernel
+    // what is left for the dynamic part: the kernel's static 128 bytes take 1024, its dynamic part being aligned to that
+    const size_t limit = static_cast<size_t>(di.smem_optin) - 1024;
+    auto region = [&](int d) {  // a warp's: d stages, pbuf, abuf, d barriers
+        return (d * static_cast<size_t>(a.stage_bytes) + 16 * G * 8 + G * 8 + 8 * d + 127) / 128 * 128;
+    };
     int nw = policy_warps(G, D), depth = 0;
     while (nw >= 1) {
-        const size_t fixed = 16 * G * 8 + G * 8 + 8 * 8;  // pbuf, abuf, up to 8 barriers
-        const size_t avail = budget > a.prefix_bytes ? budget - a.prefix_bytes : 0;
-        const size_t per_warp_avail = avail / nw;
-        depth = per_warp_avail > fixed ? static_cast<int>((per_warp_avail - fixed) / a.stage_bytes) : 0;
-        if (depth > 6) depth = 6;
+        depth = 6;
+        while (depth >= 2 && a.prefix_bytes + nw * region(depth) > limit) --depth;
         if (depth >= 2) break;
         nw >>= 1;
     }
     if (depth < 2) return fail(PKV_ERR_UNSUPPORTED, "shared memory too small for this block/head size");
     a.depth = depth;
-    const size_t fixed = 16 * G * 8 + G * 8 + 8 * static_cast<size_t>(depth);
-    a.warp_bytes = static_cast<uint32_t>(((static_cast<size_t>(depth) * a.stage_bytes + fixed + 127) / 128) * 128);
+    a.warp_bytes = static_cast<uint32_t>(region(depth));
     const size_t smem = a.prefix_bytes + static_cast<size_t>(nw) * a.warp_bytes;
 
     CUtensorMap km, vm;
