@@ -152,6 +152,16 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// Encoding needs a current context.  A host thread that has only been given pointers and a stream has none yet (the runtime
+// binds the device's at the first call that uses it): it is bound then, and the map encoded again.
+template <class Encode>
+static CUresult with_context(Encode encode) {
+    CUresult r = encode();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    return r;
+}
+
 // L2 fetch size for rows of `row_bytes` contiguous bytes: the row itself, never more.  The row of the next KV head
 // follows in memory, and a wider promotion fetches it from DRAM for a warp that does not need it (at 128-byte rows
 // 256-byte promotion read 1.42x the bytes of an INT8 decode, the neighbour head's rows mostly evicted before use).
@@ -175,9 +185,11 @@ static pkv_status cache_tensor_map(CUtensorMap* map, const void* base, const pkv
                              static_cast<cuuint64_t>(c.num_kv_heads) * c.head_dim * es};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(c.head_dim), 1u, static_cast<cuuint32_t>(c.block_size)};
     cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_NONE, promotion_for_row(static_cast<uint64_t>(c.head_dim) * es),
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = with_context([&] {
+        return enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, promotion_for_row(static_cast<uint64_t>(c.head_dim) * es),
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
     if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return PKV_OK;
 }
@@ -193,10 +205,11 @@ static pkv_status tensor_map_sw128(CUtensorMap* map, const void* base, bool fp8,
     cuuint64_t strides[2] = {d0 * es, d0 * d1 * es};
     cuuint32_t box[3] = {fp8 ? 128u : 64u, b1, b2};
     cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     promotion_for_row(fetch_bytes ? fetch_bytes : d0 * es),
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = with_context([&] {
+        return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   promotion_for_row(fetch_bytes ? fetch_bytes : d0 * es), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
     if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (swizzled) failed (%d)", static_cast<int>(r));
     return PKV_OK;
 }
