@@ -812,7 +812,7 @@ template <int G, int D, int S, class KV, class QT>
 cudaError_t launch_paged_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a, int grid,
                                 int block, size_t smem, cudaStream_t stream) {
     auto kern = paged_decode_kernel<G, D, S, KV, QT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 1024);
     if (e != cudaSuccess) return e;
     kern<<<grid, block, smem, stream>>>(kmap, vmap, a);
     return cudaGetLastError();

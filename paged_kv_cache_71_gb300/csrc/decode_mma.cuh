@@ -963,7 +963,7 @@ template <int G, int S, class KV, int HP>
 cudaError_t launch_paged_decode_prefix(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
                                        const PrefixArgs& px, int grid, int block, size_t smem, cudaStream_t stream) {
     auto kern = paged_decode_prefix_kernel<G, S, KV, HP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 256);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -983,7 +983,7 @@ template <int G, int S, class KV, int HP>
 cudaError_t launch_paged_decode_mma(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a, int grid,
                                     int block, size_t smem, cudaStream_t stream) {
     auto kern = paged_decode_mma_kernel<G, S, KV, HP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 256);
     if (e != cudaSuccess) return e;
     kern<<<grid, block, smem, stream>>>(kmap, vmap, a);
     return cudaGetLastError();

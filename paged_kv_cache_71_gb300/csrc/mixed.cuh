@@ -136,7 +136,7 @@ cudaError_t launch_paged_mixed(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                const PrefillArgs& pa, const DecodeArgs& da, const MixedArgs& ma, int grid,
                                size_t smem, cudaStream_t stream) {
     auto kern = paged_mixed_kernel<NARROW, G, KV>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 1024);
     if (e != cudaSuccess) return e;
     kern<<<grid, 384, smem, stream>>>(qmap, kmap, vmap, pa, da, ma);
     return cudaGetLastError();

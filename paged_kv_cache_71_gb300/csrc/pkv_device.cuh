@@ -16,6 +16,11 @@ namespace pkv {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// Shared memory of a block at most (227 KB).  A kernel whose dynamic part varies from call to call has its limit raised to
+// this less its static part, never to the call's own size: the limit is the process's, and another host thread's smaller call
+// would lower it between this one's raising and launching.
+constexpr int kSmemPerBlock = 227 * 1024;
+
 // Where a softmax's running maximum starts: the lowest finite value.  Scores of -inf (keys that hold infinities) then have
 // weight 2^(-inf - m) = 0 however many come first; from -inf the difference of two infinities would be no number.
 constexpr float kLowest = -3.40282347e+38f;
