@@ -160,6 +160,8 @@ pkv_status pkv_paged_attention_workspace_size(const pkv_cache_desc* cache, int32
  *        not share a workspace.
  * Supported: head_dim 64/128, block_size 4/8/16/32, G in {1, 2, 4, 8},
  *   num_seqs <= 8192.  Pointers q, out and the caches 16-byte aligned.
+ *   max_blocks_per_seq * block_size and num_seqs * max_blocks_per_seq *
+ *   num_kv_heads must stay below 2^31 (PKV_ERR_OUT_OF_RANGE otherwise).
  */
 pkv_status pkv_paged_attention_decode(void* out, const void* q, int32_t q_dtype,
                                       const void* k_cache, const void* v_cache,
@@ -286,6 +288,7 @@ pkv_status pkv_paged_prefill_varlen(void* out, const void* q, int32_t q_dtype, i
  * Supported: bf16 queries, bf16, FP8 or INT8 cache, head_dim 128,
  *   block_size 16, G in {1, 2, 4, 8}, num_seqs <= 2048, num_decode <= 8192,
  *   devices of at most 256 SMs; other cases return PKV_ERR_UNSUPPORTED.
+ *   The decode call's bounds on the table's width apply (with decode tokens).
  */
 pkv_status pkv_paged_attention_mixed(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
                                      const int32_t* cu_q, const int32_t* q_starts, const int32_t* kv_lens,
@@ -523,6 +526,10 @@ pkv_status pkv_paged_attention_decode_prefix_workspace_size(const pkv_cache_desc
  * outside the pool sets PKV_DEVERR_BAD_BLOCK.
  * Supported with cu_q: bf16 queries, bf16, FP8 or INT8 cache, head_dim 128,
  *   block_size 8/16/32, G dividing 128, num_seqs <= 2048, scale positive.
+ *   (total_q_tokens / (256 / G) + num_seqs) * num_kv_heads * (2 * key tiles of
+ *   64 in a full table row + 32) must stay below 2^31 - 4096; the shared-prefix
+ *   decode has the same bound with num_seqs tokens in num_groups runs
+ *   (PKV_ERR_OUT_OF_RANGE otherwise).
  */
 pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
                                      const int32_t* cu_q, const int32_t* kv_lens, const void* k_cache,

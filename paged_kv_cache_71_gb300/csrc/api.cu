@@ -581,6 +581,8 @@ static pkv_status decode_entry(void* out, const void* q, int32_t q_dtype, const 
     if (Hkv > 1024) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d > 1024", Hkv);
     if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq * Hkv > INT32_MAX - 64)
         return fail(PKV_ERR_OUT_OF_RANGE, "num_seqs * max_blocks_per_seq * num_kv_heads must stay below 2^31");
+    if (static_cast<int64_t>(max_blocks_per_seq) * S > INT32_MAX)  // the kernels count a row's tokens in 32 bits
+        return fail(PKV_ERR_OUT_OF_RANGE, "a row of the block table holds more than 2^31-1 tokens");
     if (!(scale == scale) || scale == 0.f) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and non-zero");
     const bool combo_ok = (q_dtype == PKV_F32 && cache->dtype == PKV_F32) ||
                           (q_dtype == PKV_BF16 && (cache->dtype == PKV_BF16 || narrow(cache->dtype)));
@@ -919,6 +921,8 @@ PKV_API pkv_status pkv_paged_attention_mixed(void* out, const void* q, int32_t q
     if (num_decode > 8192) return fail(PKV_ERR_UNSUPPORTED, "num_decode %d > 8192", num_decode);
     if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq * Hkv > INT32_MAX - 64)
         return fail(PKV_ERR_OUT_OF_RANGE, "num_seqs * max_blocks_per_seq * num_kv_heads must stay below 2^31");
+    if (num_decode > 0 && static_cast<int64_t>(max_blocks_per_seq) * S > INT32_MAX)  // the decode counts a row's tokens in 32 bits
+        return fail(PKV_ERR_OUT_OF_RANGE, "a row of the block table holds more than 2^31-1 tokens");
     if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
     if (!out || !q || !cu_q || !q_starts || !kv_lens || !k_cache || !v_cache || !block_tables)
         return fail(PKV_ERR_INVALID_ARG, "null pointer");
