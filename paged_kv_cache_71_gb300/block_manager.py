@@ -76,6 +76,39 @@ class _Seq:
     length: int = 0
 
 
+MAX_PREFIX_GROUPS = 2048  # that pkv_paged_attention_decode_prefix takes
+
+
+@dataclass
+class _Group:
+    """Neighbouring rows of a batch: their common full blocks, the sequences with tokens among them, the rows."""
+    shared: list
+    seqs: int
+    rows: int
+
+
+def _fewer_groups(groups: list[_Group]) -> list[_Group]:
+    """At most MAX_PREFIX_GROUPS groups: neighbours that share nothing as one, then the smallest savings given up."""
+    def joined(gs):
+        out: list[_Group] = []
+        for g in gs:
+            if out and not g.shared and not out[-1].shared:
+                out[-1] = _Group([], out[-1].seqs + g.seqs, out[-1].rows + g.rows)
+            else:
+                out.append(g)
+        return out
+
+    groups = joined(groups)
+    count, last = len(groups), len(groups) - 1
+    for i in sorted(range(len(groups)), key=lambda i: (groups[i].seqs - 1) * len(groups[i].shared)):
+        if count <= MAX_PREFIX_GROUPS:
+            break
+        if groups[i].shared:
+            groups[i].shared = []
+            count -= (i > 0 and not groups[i - 1].shared) + (i < last and not groups[i + 1].shared)
+    return joined(groups)
+
+
 class SequenceTables:
     """Block tables of the sequences that live in one pool, with copy-on-write."""
 
@@ -113,31 +146,33 @@ class SequenceTables:
         Neighbours whose tables start with the same full blocks are a group, so forks of one sequence and requests over
         one document should stand side by side in a batch.  A group of n over p blocks saves (n - 1) * p block reads;
         the next sequence joins it if the n + 1 of them over the c blocks that they all share save as many or more:
-        n * c >= (n - 1) * p.  A group of one shares nothing: prefix 0.
+        n * c >= (n - 1) * p.  A group of one shares nothing: prefix 0.  Sequences without tokens (finished, padding) stay
+        in the group they stand in.  More groups than the call takes (2048) are made fewer: neighbours of prefix 0 become
+        one group, then the groups that save least get prefix 0.
         """
-        cu, lens = [0], []
-        shared: list = []                                # the open group's common full blocks
-        n = 0
-
-        def close():
-            cu.append(cu[-1] + n)
-            lens.append(len(shared) * self.block_size if n > 1 else 0)
-
+        groups: list[_Group] = []
         for sid in sids:
             seq = self._seqs[sid]
             full = seq.blocks[: seq.length // self.block_size]
-            c = 0
-            while c < min(len(full), len(shared)) and full[c] == shared[c]:
-                c += 1
-            if c and n * c >= (n - 1) * len(shared):
-                shared, n = shared[:c], n + 1
-                continue
-            if n:
-                close()
-            shared, n = full, 1
-        if n:
-            close()
-        return np.asarray(cu, dtype=np.int32), np.asarray(lens, dtype=np.int32)
+            if groups:
+                g = groups[-1]
+                if seq.length == 0:
+                    g.rows += 1
+                    continue
+                c = 0
+                while c < min(len(full), len(g.shared)) and full[c] == g.shared[c]:
+                    c += 1
+                if c and g.seqs * c >= (g.seqs - 1) * len(g.shared):
+                    g.shared, g.seqs, g.rows = g.shared[:c], g.seqs + 1, g.rows + 1
+                    continue
+            groups.append(_Group(full, 1 if seq.length else 0, 1))
+        for g in groups:
+            if g.seqs < 2:
+                g.shared = []
+        if len(groups) > MAX_PREFIX_GROUPS:
+            groups = _fewer_groups(groups)
+        cu = np.cumsum([0] + [g.rows for g in groups], dtype=np.int32)
+        return cu, np.asarray([len(g.shared) * self.block_size for g in groups], dtype=np.int32)
 
     # ---- changes
     def prefill(self, sid, n_tokens: int) -> None:
