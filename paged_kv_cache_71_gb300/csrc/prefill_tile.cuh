@@ -632,7 +632,7 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
                     w1[k] = chunk(1, k);
                     amax_bits = amax4(amax4(amax_bits, w1[k]), chunk(0, k));
                 }
-                if (amax_bits >= 0x7f800000u) raise_error(a.err, PKV_DEVERR_Q_RANGE);  // inf or NaN
+                if (amax_bits >= 0x7f800000u && qi < NQ) raise_error(a.err, PKV_DEVERR_Q_RANGE);  // inf or NaN, in the chunk
                 const int ex = static_cast<int>(amax_bits >> 23) - 127;        // floor(log2(max |x|))
                 const int e = min(126, max(-126, 7 - ex));
                 const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -672,13 +672,15 @@ __device__ __forceinline__ void prefill_tile(const CUtensorMap& qmap, const CUte
             if (active && ok_q) {
                 uint8_t* qt = smem + kOffQ + 2 * t * kQHalf;
                 bool in_range = true;
+                const int chunk_rows = (NQ - qt0) * a.G;  // rows behind the chunk are copied, but are not its queries
                 for (int i = quad * 32 + lane; i < 2 * kQHalf / 16; i += kSoftmax / 2) {
+                    const bool mine = (i & (kQHalf / 16 - 1)) / 8 < chunk_rows;
                     uint4 w = *reinterpret_cast<const uint4*>(qt + i * 16);
                     uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = bf16x2_to_float2(ws[k]);
-                        in_range = in_range && fabsf(f.x) < 65520.f && fabsf(f.y) < 65520.f;
+                        in_range = in_range && (!mine || (fabsf(f.x) < 65520.f && fabsf(f.y) < 65520.f));
                         ws[k] = f16x2_rn(f.x, f.y);
                     }
                     *reinterpret_cast<uint4*>(qt + i * 16) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
