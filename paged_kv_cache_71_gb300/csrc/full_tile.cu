@@ -55,7 +55,7 @@ constexpr int kEmpty = 512;    // chunks without keys that it lists
 // one per CTA and round, so that the query tiles of one head run side by side over the same keys; what is left (an item or
 // two per CTA) is cut so that all CTAs end together.  Cut from the start, the stream's places lie anywhere in a head's keys
 // and every query tile reads them from DRAM: 3.9 GB instead of 1.3 for 12 prompts of 1000 tokens over states of 4500
-// (790 us; 717 with rounds), and 2048 rows over 8192 keys in 8 sequences 472 us instead of 430.  With shorter items the
+// (790 us; 717 with rounds; both in short loops, see kRegsSoftmax), and 2048 rows over 8192 keys in 8 sequences 472 us instead of 430.  With shorter items the
 // keys stay in L2 anyway, and the rounds' plan (4 us) is not worth it.
 constexpr int kRounds = 64;      // most rounds
 constexpr int kRoundUnits = 64;  // fewest units per item, on average
@@ -73,7 +73,8 @@ struct FullPlan {
     static constexpr int kThreads = NARROW == 2 ? 640 : 512;
     // registers per thread after the split: 256 x 176 + 256 x 80 = 256 x 184 + 256 x 72 = 512 x 128, what the launch gives;
     // 256 x 168 + 384 x 48 = 640 x 96.  bf16 168 / 176 / 184 / 192 / 200 softmax registers: cross_prompts 706 / 703 / 714 /
-    // 701 / 702 us, 256 queries over 32768 keys 206 / 203 / 209 / 207 / 207; FP8: those queries 246 / 252 / 241 / 247 / 250.
+    // 701 / 702 us (in loops below 0.1 s; 749 in loops of seconds), 256 queries over 32768 keys 206 / 203 / 209 / 207 / 207;
+    // FP8: those queries 246 / 252 / 241 / 247 / 250.
     static constexpr int kRegsSoftmax = NARROW == 2 ? 168 : NARROW == 1 ? 184 : 176;
     static constexpr int kRegsOther = NARROW == 2 ? 48 : NARROW == 1 ? 72 : 80;
 };
