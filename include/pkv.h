@@ -541,6 +541,120 @@ pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q_dtype, 
 pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
                                                     int32_t num_seqs, int32_t num_q_heads, size_t* bytes);
 
+/*
+ * Rotary positions and the cache write in one pass: the queries of this step's
+ * tokens are rotated, their keys rotated and appended to the paged cache, their
+ * values appended (pkv_reshape_and_cache with the rotation on the way).  With
+ * r = rot_dim, f_i = inv_freq[i] for i < r / 2, p = positions[t] and a =
+ * rope_scale, each pair (x, y) of the first r elements of a head becomes
+ *   (a (x cos(p f_i) - y sin(p f_i)), a (y cos(p f_i) + x sin(p f_i)))
+ * where pair i is the elements (i, i + r / 2), or (2 i, 2 i + 1) if interleaved is
+ * not 0; elements from r on are taken as they are.  The products are fp32, the
+ * angle p f_i is reduced exactly (positions of 2^31 - 1 keep full precision for
+ * frequencies below 2^24), and each result is rounded once, to the type of q_out
+ * or of the cache (as pkv_reshape_and_cache rounds it).
+ *   q, q_out: [num_tokens] rows of num_q_heads * head_dim elements, q_stride and
+ *        q_out_stride elements apart.  q_out may be q with the same stride.  Both
+ *        NULL with num_q_heads = 0: keys and values only.
+ *   k_new, v_new: [num_tokens] rows of num_kv_heads * head_dim, k_stride and
+ *        v_stride apart.  Both NULL: queries only; slot_mapping and the caches
+ *        may then be NULL.  Queries, keys and values may be parts of one row (a
+ *        fused projection's output).
+ *   positions: int32 [num_tokens], any value.
+ *   slot_mapping: as for pkv_reshape_and_cache.  Nothing is written for a token
+ *        whose slot is negative (padding) or beyond the pool
+ *        (PKV_DEVERR_BAD_SLOT): its q_out row stays too.
+ *   inv_freq: fp32 [rot_dim / 2] device array, scaled for long contexts as the
+ *        model wants it; a value that is not finite gives NaN.
+ * All tensors of src_dtype (f32 or bf16) and the caches 16-byte aligned, strides
+ * multiples of 16 bytes.
+ * Supported: rot_dim a multiple of 8 up to head_dim; the cache write's types,
+ *   head_dim 64 and 128, any head counts.
+ */
+pkv_status pkv_rope_and_cache(void* q_out, const void* q, const void* k_new, const void* v_new, int32_t src_dtype,
+                              int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                              int32_t num_q_heads, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                              float rope_scale, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                              int32_t* device_error, void* stream);
+
+/*
+ * Attention of drafted tokens (speculative decoding): sequence s owns query tokens
+ * [cu_q[s], cu_q[s + 1]), a run of n tokens whose own K/V are the last n of its
+ * kv_lens[s] cached ones (appended by this step's cache write).  Every token of the
+ * run sees the kv_lens[s] - n keys before the run, and of the run's own keys those
+ * that its mask names, so a run may hold a tree of drafts:
+ *   out = softmax(scale * q . K^T) V   over the keys that the token sees.
+ *   tree_mask: uint64 [total_q_tokens][mask_words]: bit j % 64 of word j / 64 of a
+ *        token's row says whether it sees token j of its run (itself only if its own
+ *        bit is set); bits from n on are ignored.  NULL with mask_words = 0: each
+ *        run is a chain, token i sees tokens 0 .. i.
+ * A token that sees nothing gets a zero row, and so do the tokens of a sequence with
+ * kv_lens[s] = 0 (finished, padding).  Keys and values that a token does not see do
+ * not reach its row, whatever they hold (infinities and NaN included).
+ *   cu_q: [num_seqs + 1] device int32, non-decreasing, at most total_q_tokens.  Rows
+ *        that no sequence owns are not written.
+ *   workspace: >= pkv_paged_attention_tree_workspace_size bytes, 16-byte aligned;
+ *        concurrent calls must not share it.
+ * Arithmetic: that of pkv_paged_prefill_chunk per cache type.
+ * A malformed cu_q range, a length outside [0, max_blocks_per_seq * S], one below n, or
+ * a run longer than 64 * mask_words sets PKV_DEVERR_BAD_LENGTH and leaves that
+ * sequence's rows unwritten; a table entry outside the pool sets PKV_DEVERR_BAD_BLOCK.
+ * Supported: the types, shapes and limits of pkv_paged_cross_attention with cu_q.
+ */
+pkv_status pkv_paged_attention_tree(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
+                                    const int32_t* cu_q, const int32_t* kv_lens, const uint64_t* tree_mask,
+                                    int32_t mask_words, const void* k_cache, const void* v_cache,
+                                    const pkv_cache_desc* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                    void* workspace, size_t workspace_bytes, int32_t* device_error, void* stream);
+
+/* Bytes of device workspace pkv_paged_attention_tree needs (on the current device). */
+pkv_status pkv_paged_attention_tree_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
+                                                   int32_t num_seqs, int32_t num_q_heads, size_t* bytes);
+
+/*
+ * Commit of a verified draft: the accepted path of each sequence's run, and its K/V
+ * moved to consecutive slots in every layer, in one launch without a host round trip.
+ * The run of sequence s (query tokens [cu_q[s], cu_q[s + 1]), n of them, their K/V at
+ * positions past_lens[s] + i) starts with the token that was chosen before; the others
+ * are drafts, parents[t] the index in the run of the token that t follows (-1: none),
+ * draft_tokens[t] its id, and target_tokens[t] the id that the model chose after t.
+ * The path starts with token 0; after token c comes the first token i > c with
+ * parents = c and draft_tokens = target_tokens of c, until there is none.  With m tokens
+ * path[0 .. m - 1]:
+ *   K/V       position past + path[j] -> position past + j for every j, as if in order
+ *             of j, in the k_caches[l] and v_caches[l] of all layers l < num_layers
+ *   accepted  [total_q_tokens]: path[j] at index cu_q[s] + j, -1 behind the path
+ *   num_accepted[s] = m;  seq_lens[s] = past_lens[s] + m
+ *   next_tokens[s]  target_tokens of path[m - 1], which starts the next run
+ *   keep_blocks[s] (nullable) = ceil(seq_lens[s] / S): with these, the lengths before the
+ *             commit and every finished flag set, pkv_release_sequences hands back the
+ *             blocks that the run took and the path does not need (its seq_lens, all 0,
+ *             go to scratch)
+ * A run of no tokens gives 0, past_lens[s] and next token -1.  `accepted` entries that no
+ * sequence owns are not written.
+ *   k_caches, v_caches: HOST arrays of num_layers device pointers (read during the call),
+ *        pools of the same geometry and dtype; `cache` describes one of them (its scales
+ *        are not used).
+ * The moved positions' blocks must be the sequence's own.  Output arrays must not overlap
+ * one another or the inputs.
+ * A malformed cu_q range, a run of more than PKV_MAX_COMMIT_RUN tokens, a negative length
+ * or one past max_blocks_per_seq * S with the run sets PKV_DEVERR_BAD_LENGTH; such a
+ * sequence is as one without a run (its `accepted` entries -1, where its range is one).
+ * A table entry outside the pool sets PKV_DEVERR_BAD_BLOCK and leaves the token that it
+ * concerns where it is.
+ * Supported: every cache type and shape, num_seqs <= 8192, num_layers <= PKV_MAX_LAYERS.
+ */
+#define PKV_MAX_LAYERS 128
+#define PKV_MAX_COMMIT_RUN 1024
+pkv_status pkv_commit_tree(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                           const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* cu_q, const int32_t* past_lens, const int32_t* parents,
+                           const int32_t* draft_tokens, const int32_t* target_tokens, int32_t total_q_tokens,
+                           int32_t num_seqs, int32_t* accepted, int32_t* num_accepted, int32_t* seq_lens,
+                           int32_t* next_tokens, int32_t* keep_blocks, int32_t* device_error, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* pkv_status_string(pkv_status status);
 

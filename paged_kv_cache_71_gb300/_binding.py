@@ -86,12 +86,18 @@ def lib() -> ctypes.CDLL:
     L.pkv_paged_attention_decode_prefix_workspace_size.argtypes = [D, i32, i32, ctypes.POINTER(sz)]
     L.pkv_paged_cross_attention.argtypes = [P, P, i32, i32, P, P, P, P, D, P, i32, i32, i32, f32, P, sz, P, P]
     L.pkv_paged_cross_attention_workspace_size.argtypes = [D, i32, i32, i32, ctypes.POINTER(sz)]
+    i64 = ctypes.c_int64
+    L.pkv_rope_and_cache.argtypes = [P, P, P, P, i32, i64, i64, i64, i64, P, P, i32, i32, P, i32, i32, f32, P, P, D, P, P]
+    L.pkv_paged_attention_tree.argtypes = [P, P, i32, i32, P, P, P, i32, P, P, D, P, i32, i32, i32, f32, P, sz, P, P]
+    L.pkv_paged_attention_tree_workspace_size.argtypes = [D, i32, i32, i32, ctypes.POINTER(sz)]
+    L.pkv_commit_tree.argtypes = [P, P, i32, D, P, i32, P, P, P, P, P, i32, i32, P, P, P, P, P, P, P]
     for name in ("pkv_reshape_and_cache", "pkv_paged_attention_workspace_size", "pkv_paged_attention_decode",
                  "pkv_copy_blocks", "pkv_paged_attention_decode_static_scratch", "pkv_paged_prefill_chunk",
                  "pkv_paged_prefill_varlen", "pkv_swap_blocks", "pkv_block_hashes", "pkv_extend_sequences",
                  "pkv_release_sequences", "pkv_paged_attention_decode_prefix",
                  "pkv_paged_attention_decode_prefix_workspace_size", "pkv_paged_cross_attention",
-                 "pkv_paged_cross_attention_workspace_size"):
+                 "pkv_paged_cross_attention_workspace_size", "pkv_rope_and_cache", "pkv_paged_attention_tree",
+                 "pkv_paged_attention_tree_workspace_size", "pkv_commit_tree"):
         getattr(L, name).restype = ctypes.c_int
     L.pkv_status_string.argtypes = [ctypes.c_int]
     L.pkv_status_string.restype = ctypes.c_char_p
@@ -321,6 +327,7 @@ def _refuse(func: str, device: int, device_error=None, workspace=None, **tensors
 
 _I32, _I64, _FLAG = (torch.int32,), (torch.int64,), (torch.bool, torch.uint8)
 _FLOATS = (torch.float32, torch.bfloat16)
+_MASK = (torch.int64, torch.uint64)
 
 
 def _cache_dtypes(cache: CacheDesc) -> tuple:
@@ -463,6 +470,164 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
                                          _ptr(device_error), _stream(stream, dev))
     if status:
         _check(status, "pkv_paged_cross_attention")
+
+
+def _rows(t, dtype, heads: int, D: int, tokens: int, device: int) -> bool:
+    """[tokens][heads][D] whose tokens may be further apart than a token is long (parts of a fused projection's rows)."""
+    return (t.dtype is dtype and t.shape == (tokens, heads, D) and t.get_device() == device
+            and (tokens < 2 or t.stride(0) >= heads * D) and t.stride(2) == 1 and (heads == 1 or t.stride(1) == D))
+
+
+def _refuse_rows(func: str, name: str, t, dtypes, shape) -> None:
+    if t.dtype not in dtypes:
+        raise PkvError(1, func, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() and not ((shape[0] < 2 or t.stride(0) >= shape[1] * shape[2]) and t.stride(2) == 1
+                          and (shape[1] == 1 or t.stride(1) == shape[2])):
+        raise PkvError(1, func, f"{name} must have contiguous, separate tokens (strides {t.stride()})")
+
+
+def _token_stride(t, width: int) -> int:
+    """Elements from token to token (a single token's stride may be anything)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def pkv_rope_and_cache(q_out, q, k_new, v_new, positions, slot_mapping, inv_freq, k_cache, v_cache, cache: CacheDesc,
+                       interleaved: bool = False, rope_scale: float = 1.0, device_error=None, stream=None) -> None:
+    """Rotary positions on the queries (q_out may be q) and keys, keys and values written to their slots, in one pass.
+    inv_freq: fp32, one per pair of rotated elements (rotary_frequencies makes it).  q and q_out None: keys and values only;
+    k_new and v_new None: queries only."""
+    func, L, dev, D = "pkv_rope_and_cache", lib(), _here(positions), cache.head_dim
+    if positions.dim() != 1 or inv_freq.dim() != 1:
+        _dims(func, positions=(positions, 1), inv_freq=(inv_freq, 1))
+    n, hkv, caches = positions.shape[0], cache.num_kv_heads, (cache.num_blocks, cache.block_size, cache.num_kv_heads, D)
+    some = q if q is not None else k_new
+    if some is None or (q is None) != (q_out is None) or (k_new is None) != (v_new is None):
+        raise PkvError(1, func, "q comes with q_out, k_new with v_new, and one of the pairs is needed")
+    if q is not None and q.dim() != 3:
+        _dims(func, q=(q, 3))
+    src, heads = some.dtype, 0 if q is None else q.shape[1]
+    if not (src in _FLOATS and _fits(positions, torch.int32, (n,), dev) and _fits(inv_freq, torch.float32, inv_freq.shape, dev)
+            and _word(device_error, dev) and (slot_mapping is None or _fits(slot_mapping, torch.int64, (n,), dev))
+            and (q is None or (_rows(q, src, heads, D, n, dev) and _rows(q_out, src, heads, D, n, dev)))
+            and (k_new is None or (_rows(k_new, src, hkv, D, n, dev) and _rows(v_new, src, hkv, D, n, dev)
+                                   and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and slot_mapping is not None
+                                   and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)))):
+        if k_new is not None and slot_mapping is None:
+            raise PkvError(1, func, "k_new and v_new need slot_mapping")
+        for name, t, h in (("q", q, heads), ("q_out", q_out, heads), ("k_new", k_new, hkv), ("v_new", v_new, hkv)):
+            if t is not None:
+                _refuse_rows(func, name, t, _FLOATS if t is some else (src,), (n, h, D))
+        pools = {} if k_new is None else dict(k_cache=(k_cache, _cache_dtypes(cache), caches), v_cache=(v_cache, (k_cache.dtype,), caches))
+        _refuse(func, _device(), device_error, positions=(positions, _I32, (n,)), slot_mapping=(slot_mapping, _I64, (n,)),
+                inv_freq=(inv_freq, (torch.float32,), inv_freq.shape), **pools)
+        for name, t in (("q", q), ("q_out", q_out), ("k_new", k_new), ("v_new", v_new)):
+            if t is not None and t.get_device() != _device():
+                raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
+    if n == 0:
+        return
+    qw, kw = heads * D, hkv * D
+    q_stride, q_out_stride = (0, 0) if q is None else (_token_stride(q, qw), _token_stride(q_out, qw))
+    k_stride, v_stride = (0, 0) if k_new is None else (_token_stride(k_new, kw), _token_stride(v_new, kw))
+    kc, vc = (None, None) if k_new is None else (k_cache.data_ptr(), v_cache.data_ptr())
+    status = L.pkv_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _DTYPE_CODE[src], q_out_stride, q_stride, k_stride,
+                                  v_stride, positions.data_ptr(), _ptr(slot_mapping), n, heads, inv_freq.data_ptr(),
+                                  2 * inv_freq.shape[0], int(interleaved), float(rope_scale), kc, vc, ctypes.byref(cache),
+                                  _ptr(device_error), _stream(stream, dev))
+    if status:
+        _check(status, func)
+
+
+def pkv_paged_attention_tree_workspace_size(cache: CacheDesc, total_q_tokens: int, num_seqs: int, num_q_heads: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pkv_paged_attention_tree_workspace_size(ctypes.byref(cache), int(total_q_tokens), int(num_seqs),
+                                                         int(num_q_heads), ctypes.byref(out)),
+           "pkv_paged_attention_tree_workspace_size")
+    return int(out.value)
+
+
+def pkv_paged_attention_tree(out, q, cu_q, kv_lens, tree_mask, k_cache, v_cache, cache: CacheDesc, block_tables,
+                             scale: float, workspace=None, device_error=None, stream=None) -> None:
+    """Attention of runs of drafted tokens, the last of their sequence's keys: each sees all keys before the run and those of
+    the run that its row of tree_mask (int64 or uint64 [total_q_tokens][words], bit j: token j of the run) names; tree_mask
+    None: runs are chains.  draft_tree_masks makes the masks of trees of a fixed shape."""
+    func, L, n, dev = "pkv_paged_attention_tree", lib(), kv_lens.numel(), _here(q)
+    if q.dim() != 3 or block_tables.dim() != 2 or (tree_mask is not None and tree_mask.dim() != 2):
+        _dims(func, q=(q, 3), block_tables=(block_tables, 2), **({} if tree_mask is None else dict(tree_mask=(tree_mask, 2))))
+    tokens, heads, D = q.shape
+    caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _room(workspace, dev)
+            and _word(device_error, dev)
+            and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
+            and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)
+            and _fits(block_tables, torch.int32, (n, width), dev) and _fits(kv_lens, torch.int32, (n,), dev)
+            and _fits(cu_q, torch.int32, (n + 1,), dev)
+            and (tree_mask is None or (tree_mask.dtype in _MASK and _fits(tree_mask, tree_mask.dtype, (tokens, words), dev)))):
+        caches = (*caches[:3], cache.head_dim)
+        _refuse(func, _device(), device_error, workspace, q=(q, _FLOATS, (tokens, heads, cache.head_dim)),
+                out=(out, (q.dtype,), (tokens, heads, D)), kv_lens=(kv_lens, _I32, (n,)), k_cache=(k_cache, _cache_dtypes(cache), caches),
+                v_cache=(v_cache, (k_cache.dtype,), caches), block_tables=(block_tables, _I32, (n, width)),
+                cu_q=(cu_q, _I32, (n + 1,)), tree_mask=(tree_mask, _MASK, (tokens, words)))
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = L.pkv_paged_attention_tree(out.data_ptr(), q.data_ptr(), _DTYPE_CODE[q.dtype], tokens, cu_q.data_ptr(),
+                                        kv_lens.data_ptr(), _ptr(tree_mask), words, k_cache.data_ptr(), v_cache.data_ptr(),
+                                        ctypes.byref(cache), block_tables.data_ptr(), width, n, heads, float(scale), ws, ws_bytes,
+                                        _ptr(device_error), _stream(stream, dev))
+    if status:
+        _check(status, func)
+
+
+class LayerCaches:
+    """The K and V pools of all layers of a model, checked once: alike in shape and type, contiguous, on one device."""
+
+    def __init__(self, k_caches, v_caches):
+        k_caches, v_caches = list(k_caches), list(v_caches)
+        if not k_caches or len(k_caches) != len(v_caches):
+            raise PkvError(1, "LayerCaches", f"{len(k_caches)} K and {len(v_caches)} V pools, expected as many, one or more")
+        first = k_caches[0]
+        _dims("LayerCaches", k_cache=(first, 4))
+        if first.dtype not in _DTYPE_CODE:
+            raise PkvError(1, "LayerCaches", f"pools have dtype {first.dtype}, expected a cache type")
+        for t in k_caches + v_caches:
+            if t.dtype is not first.dtype or t.shape != first.shape or t.device != first.device or not t.is_contiguous():
+                raise PkvError(1, "LayerCaches", "the layers' pools must be contiguous, of one shape, type and device")
+        self.tensors = k_caches, v_caches  # kept alive
+        self.device = first.get_device()
+        self.num_layers = len(k_caches)
+        self.desc = CacheDesc.for_cache(first)
+        array = ctypes.c_void_p * self.num_layers
+        self.k_pointers, self.v_pointers = array(*(t.data_ptr() for t in k_caches)), array(*(t.data_ptr() for t in v_caches))
+
+
+def pkv_commit_tree(layers: LayerCaches, block_tables, cu_q, past_lens, parents, draft_tokens, target_tokens, accepted,
+                    num_accepted, seq_lens, next_tokens, keep_blocks=None, device_error=None, stream=None) -> None:
+    """The accepted path of each sequence's draft tree (accepted, num_accepted, seq_lens, next_tokens, keep_blocks are written),
+    its K/V moved to consecutive slots in all layers."""
+    func, L, dev, i32 = "pkv_commit_tree", lib(), _here(past_lens), torch.int32
+    if past_lens.dim() != 1 or block_tables.dim() != 2 or parents.dim() != 1:
+        _dims(func, past_lens=(past_lens, 1), block_tables=(block_tables, 2), parents=(parents, 1))
+    shape, runs, width = past_lens.shape, parents.shape, block_tables.shape[1]
+    n, tokens = shape[0], runs[0]
+    if not (layers.device == dev and _word(device_error, dev) and _fits(past_lens, i32, shape, dev)
+            and _fits(block_tables, i32, (n, width), dev) and _fits(cu_q, i32, (n + 1,), dev) and _fits(parents, i32, runs, dev)
+            and _fits(draft_tokens, i32, runs, dev) and _fits(target_tokens, i32, runs, dev) and _fits(accepted, i32, runs, dev)
+            and _fits(num_accepted, i32, shape, dev) and _fits(seq_lens, i32, shape, dev) and _fits(next_tokens, i32, shape, dev)
+            and (keep_blocks is None or _fits(keep_blocks, i32, shape, dev))):
+        _refuse(func, _device(), device_error, past_lens=(past_lens, _I32, (n,)), block_tables=(block_tables, _I32, (n, width)),
+                cu_q=(cu_q, _I32, (n + 1,)), parents=(parents, _I32, (tokens,)), draft_tokens=(draft_tokens, _I32, (tokens,)),
+                target_tokens=(target_tokens, _I32, (tokens,)), accepted=(accepted, _I32, (tokens,)),
+                num_accepted=(num_accepted, _I32, (n,)), seq_lens=(seq_lens, _I32, (n,)), next_tokens=(next_tokens, _I32, (n,)),
+                keep_blocks=(keep_blocks, _I32, (n,)))
+        raise PkvError(1, func, f"the layers' pools are on device {layers.device}, not on the current CUDA device")
+    status = L.pkv_commit_tree(layers.k_pointers, layers.v_pointers, layers.num_layers, ctypes.byref(layers.desc),
+                               block_tables.data_ptr(), width, cu_q.data_ptr(), past_lens.data_ptr(), parents.data_ptr(),
+                               draft_tokens.data_ptr(), target_tokens.data_ptr(), tokens, n, accepted.data_ptr(),
+                               num_accepted.data_ptr(), seq_lens.data_ptr(), next_tokens.data_ptr(), _ptr(keep_blocks),
+                               _ptr(device_error), _stream(stream, dev))
+    if status:
+        _check(status, func)
 
 
 def pkv_status_string(status: int) -> str:

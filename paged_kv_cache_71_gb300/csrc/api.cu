@@ -9,11 +9,13 @@
 #include <mutex>
 
 #include "cache_ops.cuh"
+#include "commit.cuh"
 #include "decode.cuh"
 #include "decode_mma.cuh"
 #include "full_tile.cuh"
 #include "mixed.cuh"
 #include "prefill.cuh"
+#include "rope.cuh"
 #include "tables.cuh"
 
 namespace pkv {
@@ -1421,6 +1423,69 @@ PKV_API pkv_status pkv_paged_attention_decode_prefix(void* out, const void* q, i
     return PKV_OK;
 }
 
+// Runs of query tokens (cu_q) over paged keys: cross attention, and with `tree` the runs whose tokens are the last keys.
+static pkv_status stream_entry(const char* what, void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
+                               const int32_t* cu_q, const int32_t* kv_lens, const void* k_cache, const void* v_cache,
+                               const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+                               int32_t* device_error, void* stream, bool tree = false, const uint64_t* tree_mask = nullptr,
+                               int32_t mask_words = 0) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (total_q_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (total_q_tokens=%d num_seqs=%d num_q_heads=%d max_blocks_per_seq=%d)",
+                    total_q_tokens, num_seqs, num_q_heads, max_blocks_per_seq);
+    int G;
+    if ((st = check_full(what, q_dtype, *cache, num_q_heads, 128, &G)) != PKV_OK) return st;
+    if (num_seqs > prefill_ws_max_seqs())
+        return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > %d sequences per call", num_seqs, prefill_ws_max_seqs());
+    if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq > INT32_MAX ||
+        static_cast<int64_t>(max_blocks_per_seq) * cache->block_size > INT32_MAX - 64)
+        return fail(PKV_ERR_OUT_OF_RANGE, "block table larger than 2^31-1 entries or 2^31-65 tokens a row");
+    if (!(scale > 0.f && scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and positive");
+    if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
+    if (!out || !q || !cu_q || !kv_lens || !k_cache || !v_cache || !block_tables)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PKV_ERR_INVALID_ARG, "q, out and the caches must be 16-byte aligned");
+    if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_tables))
+        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, cache->dtype, false);
+    if (!workspace || workspace_bytes < fs.total)
+        return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", fs.total,
+                    workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    const int nk = narrow_kind(cache->dtype);
+    if (static_cast<size_t>(di.smem_optin) < paged_full_smem_bytes(nk, tree))
+        return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the %s tile", what);
+    uint8_t* q_ops = full_base(workspace) + fs.q_ops;
+    PrefillArgs pa;
+    CUtensorMap qm, km, vm;
+    if ((st = full_setup(&pa, &qm, &km, &vm, out, nk ? q_ops : q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
+                         num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
+        return st;
+    FullArgs fa = full_args(fs, workspace, nullptr, 0);
+    fa.tree = tree;
+    fa.tree_mask = tree_mask;
+    fa.mask_words = mask_words;
+    fa.v_cache = v_cache;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (nk) {
+        e = launch_full_prepare(q, q_ops, const_cast<float*>(fa.q_scale), static_cast<int64_t>(total_q_tokens) * num_q_heads,
+                                nullptr, 0, nk, di.sms, s);
+        if (e != cudaSuccess) return cuda_fail(e, what);
+    }
+    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, nk != 0, s);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    e = launch_join_cuts(pa, fa, di.sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return PKV_OK;
+}
+
 PKV_API pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
                                                             int32_t num_seqs, int32_t num_q_heads, size_t* bytes) {
     g_detail[0] = 0;
@@ -1456,54 +1521,163 @@ PKV_API pkv_status pkv_paged_cross_attention(void* out, const void* q, int32_t q
         return decode_entry(out, q, q_dtype, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, kv_lens,
                             num_seqs, num_q_heads, scale, 0, 0, workspace, workspace_bytes, device_error, stream, false);
     }
+    return stream_entry("cross attention", out, q, q_dtype, total_q_tokens, cu_q, kv_lens, k_cache, v_cache, cache, block_tables,
+                        max_blocks_per_seq, num_seqs, num_q_heads, scale, workspace, workspace_bytes, device_error, stream);
+}
+
+// ------------------------------------------------------------------ drafted tokens: attention, rotary append, commit
+
+PKV_API pkv_status pkv_paged_attention_tree_workspace_size(const pkv_cache_desc* cache, int32_t total_q_tokens,
+                                                           int32_t num_seqs, int32_t num_q_heads, size_t* bytes) {
     g_detail[0] = 0;
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
-    if (total_q_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0)
-        return fail(PKV_ERR_INVALID_ARG, "bad sizes (total_q_tokens=%d num_seqs=%d num_q_heads=%d max_blocks_per_seq=%d)",
-                    total_q_tokens, num_seqs, num_q_heads, max_blocks_per_seq);
-    int G;
-    if ((st = check_full("cross attention", q_dtype, *cache, num_q_heads, 128, &G)) != PKV_OK) return st;
-    if (num_seqs > prefill_ws_max_seqs())
-        return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > %d sequences per call", num_seqs, prefill_ws_max_seqs());
-    if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq > INT32_MAX ||
-        static_cast<int64_t>(max_blocks_per_seq) * cache->block_size > INT32_MAX - 64)
-        return fail(PKV_ERR_OUT_OF_RANGE, "block table larger than 2^31-1 entries or 2^31-65 tokens a row");
-    if (!(scale > 0.f && scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and positive");
-    if (num_seqs == 0 || total_q_tokens == 0) return PKV_OK;
-    if (!out || !q || !kv_lens || !k_cache || !v_cache || !block_tables)
-        return fail(PKV_ERR_INVALID_ARG, "null pointer");
-    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
-        return fail(PKV_ERR_INVALID_ARG, "q, out and the caches must be 16-byte aligned");
-    if (!aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_tables))
-        return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    if (!bytes) return fail(PKV_ERR_INVALID_ARG, "bytes is NULL");
+    if (total_q_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (total_q_tokens=%d num_seqs=%d num_q_heads=%d num_kv_heads=%d)",
+                    total_q_tokens, num_seqs, num_q_heads, cache->num_kv_heads);
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;
-    const FullScratch fs = full_scratch(di.sms, total_q_tokens, num_q_heads, cache->dtype, false);
-    if (!workspace || workspace_bytes < fs.total)
-        return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", fs.total,
-                    workspace ? workspace_bytes : static_cast<size_t>(0));
-    if (!aligned16(workspace)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
-    const int nk = narrow_kind(cache->dtype);
-    if (static_cast<size_t>(di.smem_optin) < paged_full_smem_bytes(nk))
-        return fail(PKV_ERR_UNSUPPORTED, "device shared memory too small for the cross-attention tile");
-    uint8_t* q_ops = full_base(workspace) + fs.q_ops;
-    PrefillArgs pa;
-    CUtensorMap qm, km, vm;
-    if ((st = full_setup(&pa, &qm, &km, &vm, out, nk ? q_ops : q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
-                         num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
-        return st;
-    const FullArgs fa = full_args(fs, workspace, nullptr, 0);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (nk) {
-        e = launch_full_prepare(q, q_ops, const_cast<float*>(fa.q_scale), static_cast<int64_t>(total_q_tokens) * num_q_heads,
-                                nullptr, 0, nk, di.sms, s);
-        if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention preparation launch");
+    *bytes = full_scratch(di.sms, total_q_tokens, num_q_heads, cache->dtype, false).total;
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_paged_attention_tree(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
+                                            const int32_t* cu_q, const int32_t* kv_lens, const uint64_t* tree_mask,
+                                            int32_t mask_words, const void* k_cache, const void* v_cache,
+                                            const pkv_cache_desc* cache, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                            void* workspace, size_t workspace_bytes, int32_t* device_error, void* stream) {
+    g_detail[0] = 0;
+    if (tree_mask ? mask_words < 1 || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) : mask_words != 0)
+        return fail(PKV_ERR_INVALID_ARG, "tree_mask: 8-byte aligned with mask_words (%d) of at least 1, or NULL with 0", mask_words);
+    return stream_entry("tree attention", out, q, q_dtype, total_q_tokens, cu_q, kv_lens, k_cache, v_cache, cache, block_tables,
+                        max_blocks_per_seq, num_seqs, num_q_heads, scale, workspace, workspace_bytes, device_error, stream, true,
+                        tree_mask, mask_words);
+}
+
+PKV_API pkv_status pkv_rope_and_cache(void* q_out, const void* q, const void* k_new, const void* v_new, int32_t src_dtype,
+                                      int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                      const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                      int32_t num_q_heads, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                      float rope_scale, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                                      int32_t* device_error, void* stream) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_q_heads < 0)
+        return fail(PKV_ERR_INVALID_ARG, "bad sizes (num_tokens=%d num_q_heads=%d)", num_tokens, num_q_heads);
+    if (src_dtype != PKV_F32 && src_dtype != PKV_BF16)
+        return fail(PKV_ERR_UNSUPPORTED, "source dtype %d (supported: f32, bf16)", src_dtype);
+    if (rot_dim <= 0 || rot_dim > cache->head_dim || rot_dim % 8 != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "rot_dim %d (supported: multiples of 8 up to head_dim %d)", rot_dim, cache->head_dim);
+    if (!(rope_scale > 0.f && rope_scale < 3.0e38f)) return fail(PKV_ERR_INVALID_ARG, "rope_scale must be finite and positive");
+    if (!q != (num_q_heads == 0) || !q_out != !q)
+        return fail(PKV_ERR_INVALID_ARG, "q and q_out come with num_q_heads, or NULL with 0");
+    if (!k_new != !v_new) return fail(PKV_ERR_INVALID_ARG, "k_new and v_new come together or not at all");
+    if (num_tokens == 0 || (!q && !k_new)) return PKV_OK;
+    if (!positions || !inv_freq || (k_new && (!slot_mapping || !k_cache || !v_cache)))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PKV_ERR_INVALID_ARG, "q, q_out, k_new, v_new and the caches must be 16-byte aligned");
+    const int64_t row = 16 / elem_bytes(src_dtype), Dh = cache->head_dim;
+    const int Hkv = k_new ? cache->num_kv_heads : 0;
+    if ((q && (q_stride % row || q_out_stride % row || q_stride < num_q_heads * Dh || q_out_stride < num_q_heads * Dh)) ||
+        (k_new && (k_stride % row || v_stride % row || k_stride < Hkv * Dh || v_stride < Hkv * Dh)))
+        return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes and hold a token's heads");
+    if (!aligned4(positions) || !aligned4(inv_freq) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return fail(PKV_ERR_INVALID_ARG, "positions and inv_freq must be 4-byte aligned, slot_mapping 8-byte");
+    if (static_cast<int64_t>(num_q_heads) + 2ll * Hkv > INT32_MAX / 2)
+        return fail(PKV_ERR_OUT_OF_RANGE, "num_q_heads %d", num_q_heads);
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    RopeArgs a;
+    a.q = static_cast<const uint8_t*>(q);
+    a.k = static_cast<const uint8_t*>(k_new);
+    a.v = static_cast<const uint8_t*>(v_new);
+    a.q_out = static_cast<uint8_t*>(q_out);
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.inv_freq = inv_freq;
+    a.factor = rope_scale;
+    a.tokens = num_tokens;
+    a.Hq = num_q_heads;
+    a.Hkv = Hkv;
+    a.d_shift = cache->head_dim == 64 ? 6 : 7;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.pool_slots = static_cast<int64_t>(cache->num_blocks) * cache->block_size;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.k_head = cache->k_head_scales;
+    a.v_head = cache->v_head_scales;
+    a.err = device_error;
+    const cudaError_t e = launch_rope_and_cache(a, src_dtype, cache->dtype, di.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope_and_cache launch");
+    return PKV_OK;
+}
+
+PKV_API pkv_status pkv_commit_tree(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                                   const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* cu_q, const int32_t* past_lens, const int32_t* parents,
+                                   const int32_t* draft_tokens, const int32_t* target_tokens, int32_t total_q_tokens,
+                                   int32_t num_seqs, int32_t* accepted, int32_t* num_accepted, int32_t* seq_lens,
+                                   int32_t* next_tokens, int32_t* keep_blocks, int32_t* device_error, void* stream) {
+    g_detail[0] = 0;
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if ((st = check_tables(max_blocks_per_seq, num_seqs, cache->block_size, cache->num_blocks)) != PKV_OK) return st;
+    if (total_q_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "total_q_tokens %d < 0", total_q_tokens);
+    if (num_layers < 1) return fail(PKV_ERR_INVALID_ARG, "num_layers %d < 1", num_layers);
+    if (num_layers > kMaxLayers) return fail(PKV_ERR_UNSUPPORTED, "num_layers %d > %d", num_layers, kMaxLayers);
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_caches || !v_caches || !block_tables || !cu_q || !past_lens || !num_accepted || !seq_lens || !next_tokens ||
+        (total_q_tokens > 0 && (!parents || !draft_tokens || !target_tokens || !accepted)))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    for (const void* p : {static_cast<const void*>(block_tables), static_cast<const void*>(cu_q), static_cast<const void*>(past_lens),
+                          static_cast<const void*>(parents), static_cast<const void*>(draft_tokens),
+                          static_cast<const void*>(target_tokens), static_cast<const void*>(accepted),
+                          static_cast<const void*>(num_accepted), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(next_tokens), static_cast<const void*>(keep_blocks)})
+        if (!aligned4(p)) return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    if (seq_lens == past_lens) return fail(PKV_ERR_INVALID_ARG, "seq_lens must not be past_lens");
+    CommitArgs a;
+    for (int l = 0; l < num_layers; ++l) {
+        if (!k_caches[l] || !v_caches[l]) return fail(PKV_ERR_INVALID_ARG, "null cache pointer (layer %d)", l);
+        if (!aligned16(k_caches[l]) || !aligned16(v_caches[l]))
+            return fail(PKV_ERR_INVALID_ARG, "caches must be 16-byte aligned (layer %d)", l);
+        a.k[l] = static_cast<uint4*>(k_caches[l]);
+        a.v[l] = static_cast<uint4*>(v_caches[l]);
     }
-    e = launch_paged_full(qm, km, vm, pa, fa, nk, di.sms, nk != 0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention launch");
-    e = launch_join_cuts(pa, fa, di.sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "paged_cross_attention join launch");
+    const int64_t vecs = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim * elem_bytes(cache->dtype) / 16;
+    if (vecs * 2 * num_layers > INT32_MAX / 2) return fail(PKV_ERR_OUT_OF_RANGE, "num_kv_heads %d", cache->num_kv_heads);
+    DeviceInfo di;
+    if ((st = device_info(&di)) != PKV_OK) return st;
+    a.tables = block_tables;
+    a.cu_q = cu_q;
+    a.past_lens = past_lens;
+    a.parents = parents;
+    a.draft = draft_tokens;
+    a.target = target_tokens;
+    a.accepted = accepted;
+    a.num_accepted = num_accepted;
+    a.seq_lens = seq_lens;
+    a.next_tokens = next_tokens;
+    a.keep_blocks = keep_blocks;
+    a.err = device_error;
+    a.layers = num_layers;
+    a.MB = max_blocks_per_seq;
+    a.shift = log2_of(cache->block_size);
+    a.NB = cache->num_blocks;
+    a.tokens = total_q_tokens;
+    a.vecs = static_cast<int>(vecs);
+    const cudaError_t e = launch_commit_tree(a, num_seqs, di.sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "commit_tree launch");
     return PKV_OK;
 }

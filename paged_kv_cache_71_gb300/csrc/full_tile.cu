@@ -1,5 +1,6 @@
 // full_tile.cu -- attention of many query rows over a paged K/V range without a mask: cross attention to an encoder's
-// states (pkv_paged_cross_attention) and the shared prefixes of a decode batch (pkv_paged_attention_decode_prefix).
+// states (pkv_paged_cross_attention) and the shared prefixes of a decode batch (pkv_paged_attention_decode_prefix); and with
+// a mask over the last keys, those of the query tokens themselves: trees of drafted tokens (pkv_paged_attention_tree, TREE).
 //
 // Chunks and items are described in full_tile.cuh.  An item reads its keys once for all of its rows, in tiles of 64:
 // S = Q K^T, P = 2^(S - m) with the running maximum m (log2 units), O += P V.
@@ -98,7 +99,10 @@ constexpr int kFMlOut = kFItems + 32 * kBatch;      // (m, l) of the other group
 constexpr int kFUnits = kFMlOut + 2 * 128 * 8;      // the chunks' first units, [kMaxSeqs + 1]
 constexpr int kFFirst = kFUnits + 4 * (kMaxSeqs + 1);  // and first items
 constexpr int kFEnd = kFFirst + 4 * (kMaxSeqs + 1);
-static_assert(kFMine + 52 <= kFItems, "meta slots overlap");
+static_assert(kFMine + 56 <= kFItems, "meta slots overlap");
+constexpr int kFOwn = kFEnd;                        // TREE: the listed items' runs, int2 {first token, keys before its own}
+constexpr int kFTreeEnd = kFOwn + 8 * kBatch;
+static_assert(kFOwn % 8 == 0, "int2 alignment");
 
 // One CTA's part of an item
 struct Item {
@@ -144,7 +148,70 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, uint64_t 
 
 }  // namespace
 
+// One word of values (two bf16, four E4M3 codes) with those that are infinite or no numbers as 0.
 template <int NARROW>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+    if constexpr (NARROW == 1) {  // 0x7f, 0xff
+        const uint32_t odd = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+        return w & ~(odd * 0xffu);
+    }
+    const uint32_t odd = (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15;
+    return w & ~(odd * 0xffffu);
+}
+
+// Keys whose position is in [base, base + 64) that a token sees, as bits.  own: its run's first token and the keys before the
+// run's own; tok: the token; keys: of the sequence.  Without a mask the run is a chain: every token sees those up to itself.
+__device__ __forceinline__ uint64_t visible(const FullArgs& f, int2 own, int tok, int base, int keys) {
+    const int rel = base - own.y;  // base in the run
+    uint64_t w;
+    if (f.tree_mask == nullptr) {
+        const int n = tok - own.x - rel + 1;
+        w = n >= 64 ? ~0ull : n > 0 ? (1ull << n) - 1 : 0ull;
+    } else {
+        const uint64_t* m = f.tree_mask + static_cast<size_t>(tok) * f.mask_words;
+        if (rel >= 0) {
+            const int i = rel >> 6, sh = rel & 63;
+            w = i < f.mask_words ? __ldg(m + i) >> sh : 0ull;
+            if (sh && i + 1 < f.mask_words) w |= __ldg(m + i + 1) << (64 - sh);
+        } else {  // (base + 64 > own.y: rel > -64)
+            w = (__ldg(m) << -rel) | ((1ull << -rel) - 1);
+        }
+    }
+    const int left = keys - base;
+    return left < 64 ? w & ((1ull << left) - 1) : w;
+}
+
+// TREE: values of the run's own keys that are infinite or no numbers were zeroed, since 0 times them is no number and most rows
+// see only some of these keys.  Added here to what is stored of a row that does see them (its record, or where rec is NULL its
+// output): only where a CTA met any.
+template <int NARROW>
+__device__ __noinline__ void add_odd(const PrefillArgs& a, const FullArgs& f, const Item& it, int2 own, int tok, int h, float* rec,
+                                     __nv_bfloat16* out) {
+    const int end = min(it.keys, (it.j0 + it.n) * kKeys);
+#pragma unroll 1
+    for (int p = max(own.y, it.j0 * kKeys); p < end; ++p) {
+        const int base = p & ~(kKeys - 1);
+        if (!(visible(f, own, tok, base, it.keys) >> (p - base) & 1)) continue;
+        const int b = a.block_table[static_cast<size_t>(it.table) + p / a.S];
+        if (b < 0 || b >= a.NB) continue;
+        const size_t at = ((static_cast<size_t>(b) * a.S + p % a.S) * a.Hkv + h) * 128;
+#pragma unroll 1
+        for (int d = 0; d < 128; ++d) {
+            float x = __int_as_float(0x7fc00000);
+            if constexpr (NARROW == 1) {
+                if ((static_cast<const uint8_t*>(f.v_cache)[at + d] & 0x7f) != 0x7f) continue;
+            } else {
+                const uint32_t w = static_cast<const uint16_t*>(f.v_cache)[at + d];
+                if ((w & 0x7f80u) != 0x7f80u) continue;
+                x = __uint_as_float(w << 16);
+            }
+            if (rec) rec[d] += x;
+            else out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
+        }
+    }
+}
+
+template <int NARROW, bool TREE>
 __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     paged_full_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const PrefillArgs a, const FullArgs f) {
@@ -162,6 +229,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     volatile int* mine = reinterpret_cast<volatile int*>(meta + kFMine);
     Item* items = reinterpret_cast<Item*>(meta + kFItems);
     float2* ml_out = reinterpret_cast<float2*>(meta + kFMlOut);
+    int2* own = reinterpret_cast<int2*>(meta + kFOwn);  // TREE only
     int* empty = reinterpret_cast<int*>(ml_out);  // while the plan is made: chunks without keys
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, ncta = gridDim.x;
@@ -183,6 +251,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         mine[11] = 0;
+        if constexpr (TREE) mine[13] = 0;
         prefetch_tensormap(&qmap);
     }
     if (warp == 8 && lane == 0) prefetch_tensormap(&kmap);
@@ -198,7 +267,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         Chunk k;
         const int q0 = a.cu_q[c], q1 = a.cu_q[c + 1], kv = a.kv_lens[c];
         const bool bad_q = q0 < 0 || q1 < q0 || q1 > a.NQ;
-        const bool bad = bad_q || kv < 0 || kv > a.MB * a.S || (f.prefix && (kv & (a.S - 1)) != 0);
+        bool bad = bad_q || kv < 0 || kv > a.MB * a.S || (f.prefix && (kv & (a.S - 1)) != 0);
+        if constexpr (TREE) bad = bad || (kv > 0 && (kv < q1 - q0 || (f.tree_mask && q1 - q0 > f.mask_words * 64ll)));
         if (bad && report) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
         k.q0 = bad_q ? 0 : q0;
         k.tokens = bad_q ? 0 : q1 - q0;
@@ -225,6 +295,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
         it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
         items[slot] = it;
+        if constexpr (TREE) own[slot] = make_int2(k.q0, k.keys - k.tokens);
         if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk + item_units(k.w), Uk + k.ku) : make_int4(0, 0, 0, 0);
     };
     // Items of a chunk that start before x1, but the last of them if x1 is among its first units.
@@ -639,6 +710,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     const int step = pair ? 1 : 2;
                     int x = g + first_tile(t, i, pair);
                     const int x0 = x;
+                    // TREE: the first key tile (of the CTA's count) with keys that some row does not see
+                    const int masked = TREE ? g + (own[i].y >> 6) - items[i].j0 : 0;
 #pragma unroll 1
                     for (; g < end && ok; ++g) {
                         const int st = g % kStages, b = c & 1;
@@ -647,10 +720,12 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                             if (ok && lane == 0) mbar_arrive(bar + 8 * (kFVEmpty + st));
                             continue;
                         }
-                        if (NARROW != 2 && g == end - 1 && last_keys < kKeys) {
+                        if (NARROW != 2 && (TREE ? g >= masked : g == end - 1 && last_keys < kKeys)) {
                             // V rows past the last key are not data, and 0 times what they hold may be NaN (an INT8 code is
-                            // a number): the softmax group zeroes them, of an item of two query tiles group A
-                            if (!pair || t == 0) {
+                            // a number): the softmax group zeroes them, of an item of two query tiles group A.  (TREE: also
+                            // what is no finite number in the rows of the run's own keys, and each group for itself: there can
+                            // be several such tiles, and A could be two phases of kFZero ahead of B.)
+                            if (TREE || !pair || t == 0) {
                                 if (ok && lane == 0) {
                                     mine[8 + t] = st;
                                     mbar_arrive(bar + 8 * (kFVThere + t));
@@ -774,6 +849,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 const bool valid = row < it.tokens * a.G;
                 const bool live = (row & ~31) < it.tokens * a.G;  // some row of this warp is the item's
                 const int h = it.head_pair & 0xffff;
+                const int2 run = TREE ? own[i] : make_int2(0, 0);
                 const size_t tok_row = (static_cast<size_t>(it.q_row) + (row >> g_shift)) * a.Hq + (static_cast<size_t>(h) << g_shift) +
                                        (row & (a.G - 1));
                 float m_ref = kLowest, l_run = 0.f;
@@ -803,7 +879,15 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     if (live) {
                         float v[64];
                         tmem_ld64(tS, v);
-                        if (left < kKeys) {  // keys past the last: their probabilities come out as 0
+                        if constexpr (TREE) {
+                            const int base = it.keys - left;
+                            if (base + kKeys > run.y) {  // keys that are not seen: their probabilities come out as 0
+                                const uint64_t see = visible(f, run, it.q_row + min(row >> g_shift, it.tokens - 1), base, it.keys);
+                                const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+                                for (int u = 0; u < 64; ++u) v[u] = (u < 32 ? lo >> u : hi >> (u - 32)) & 1u ? v[u] : -INFINITY;
+                            }
+                        } else if (left < kKeys) {  // keys past the last: their probabilities come out as 0
 #pragma unroll
                             for (int u = 0; u < 64; ++u) v[u] = u < left ? v[u] : -INFINITY;
                         }
@@ -861,21 +945,35 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         }
                     }
                     // V rows past the last key: zero, once they have landed
-                    if (NARROW != 2 && left < kKeys && (t == 0 || !pair)) {
+                    if (NARROW != 2 && (TREE ? it.keys - left + kKeys > run.y : left < kKeys) && (TREE || t == 0 || !pair)) {
                         if (!warp_wait(bar + 8 * (kFVThere + t), zeroed++ & 1, a.timeout_ns)) {
                             give_up();
                             break;
                         }
                         const int st = mine[8 + t];
                         constexpr int kRowChunks = NARROW == 1 ? 8 : 16;  // 16-byte pieces of a key's row
+                        const int from = TREE ? max(0, run.y - (it.keys - left)) : left;  // the first row to look at
 #pragma unroll 1
-                        for (int u = r; u < (kKeys - left) * kRowChunks; u += 128) {
-                            const int key = left + u / kRowChunks, k = u % kRowChunks;
-                            *reinterpret_cast<uint4*>(smem + PL::kOffV + st * kStage + (k >> 3) * kKvHalf + key * 128 +
-                                                      (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int u = r; u < (kKeys - from) * kRowChunks; u += 128) {
+                            const int key = from + u / kRowChunks, k = u % kRowChunks;
+                            uint4* at = reinterpret_cast<uint4*>(smem + PL::kOffV + st * kStage + (k >> 3) * kKvHalf + key * 128 +
+                                                                 (k & 7) * 16);
+                            if (TREE && key < left) {
+                                // a value that is no finite number goes to the rows that see it at the item's end
+                                const uint4 was = *at;
+                                const uint4 is = make_uint4(finite_or_zero<NARROW>(was.x), finite_or_zero<NARROW>(was.y),
+                                                            finite_or_zero<NARROW>(was.z), finite_or_zero<NARROW>(was.w));
+                                if (is.x != was.x || is.y != was.y || is.z != was.z || is.w != was.w) {
+                                    mine[13] = 1;
+                                    __threadfence_block();
+                                    *at = is;
+                                }
+                            } else {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
                         fence_proxy_async_smem();
-                        if (pair) mbar_arrive(bar + 8 * kFZero);
+                        if (!TREE && pair) mbar_arrive(bar + 8 * kFZero);
                     }
                     if (lent) {  // the P V that this P leads to overwrites O: the other group has read it
                         lent = false;
@@ -952,6 +1050,9 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         __syncwarp();  // TMEM is read by whole warps: the rows that are none wait for the others
                     }
                     if (rec && valid) f.rec_ml[rec_row] = make_float2(m_ref, l_run);
+                    if (TREE && NARROW != 2 && valid && mine[13])
+                        add_odd<NARROW>(a, f, it, run, it.q_row + (row >> g_shift), h, rec ? rec_o : nullptr,
+                                        reinterpret_cast<__nv_bfloat16*>(out_o));
                 }
                 tc_fence_before();  // the next item's first P V overwrites O, once this group's P of it is there
                 if (split) mbar_arrive(bar + 8 * (kFTaken + t));
@@ -1084,12 +1185,15 @@ __global__ void __launch_bounds__(256) full_prepare_kernel(const uint2* __restri
     }
 }
 
-template <int NARROW>
+template <int NARROW, bool TREE>
 static size_t full_smem() {
-    return static_cast<size_t>(FullPlan<NARROW>::kOffMeta) + kFEnd + 1024;
+    return static_cast<size_t>(FullPlan<NARROW>::kOffMeta) + (TREE ? kFTreeEnd : kFEnd) + 1024;
 }
 
-size_t paged_full_smem_bytes(int narrow) { return narrow == 2 ? full_smem<2>() : narrow == 1 ? full_smem<1>() : full_smem<0>(); }
+size_t paged_full_smem_bytes(int narrow, bool tree) {
+    if (tree) return narrow == 2 ? full_smem<2, true>() : narrow == 1 ? full_smem<1, true>() : full_smem<0, true>();
+    return narrow == 2 ? full_smem<2, false>() : narrow == 1 ? full_smem<1, false>() : full_smem<0, false>();
+}
 
 cudaError_t launch_full_prepare(const void* q, void* ops, float* scale, int64_t rows, int* counters, int64_t n_counters,
                                 int narrow, int sms, cudaStream_t stream) {
@@ -1103,11 +1207,11 @@ cudaError_t launch_full_prepare(const void* q, void* ops, float* scale, int64_t 
     return cudaGetLastError();
 }
 
-template <int NARROW>
+template <int NARROW, bool TREE>
 static cudaError_t launch_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const PrefillArgs& a, const FullArgs& f, int grid, bool prepared, cudaStream_t stream) {
-    const size_t smem = full_smem<NARROW>();
-    auto kern = paged_full_kernel<NARROW>;
+    const size_t smem = full_smem<NARROW, TREE>();
+    auto kern = paged_full_kernel<NARROW, TREE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1126,10 +1230,13 @@ static cudaError_t launch_full(const CUtensorMap& qmap, const CUtensorMap& kmap,
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const PrefillArgs& a, const FullArgs& f, int narrow, int grid, bool prepared,
                               cudaStream_t stream) {
-    switch (narrow) {
-        case 0: return launch_full<0>(qmap, kmap, vmap, a, f, grid, prepared, stream);
-        case 1: return launch_full<1>(qmap, kmap, vmap, a, f, grid, prepared, stream);
-        case 2: return launch_full<2>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+    switch (narrow + (f.tree ? 3 : 0)) {
+        case 0: return launch_full<0, false>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 1: return launch_full<1, false>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 2: return launch_full<2, false>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 3: return launch_full<0, true>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 4: return launch_full<1, true>(qmap, kmap, vmap, a, f, grid, prepared, stream);
+        case 5: return launch_full<2, true>(qmap, kmap, vmap, a, f, grid, prepared, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -1,5 +1,5 @@
-// full_tile.cuh -- arguments and launchers of the unmasked attention stream (full_tile.cu): cross attention, and the
-// shared prefixes of a decode batch.
+// full_tile.cuh -- arguments and launchers of the attention stream (full_tile.cu): cross attention, the shared prefixes of a
+// decode batch, and runs of drafted tokens over their sequence's cache.
 #pragma once
 
 #include "prefill.cuh"
@@ -8,7 +8,8 @@ namespace pkv {
 
 // Chunks, each a run of query tokens and the keys they all attend to:
 //   cross attention: sequence s, query tokens [cu_q[s], cu_q[s + 1]), keys [0, kv_lens[s]) of table row s;
-//   shared prefixes: group g, tokens = sequences [cu_q[g], cu_q[g + 1]), keys [0, kv_lens[g]) of its first sequence's row.
+//   shared prefixes: group g, tokens = sequences [cu_q[g], cu_q[g + 1]), keys [0, kv_lens[g]) of its first sequence's row;
+//   draft trees: as cross attention, but the run's tokens are the last of the keys, and each sees those that its mask names.
 // An item is one or two query tiles (128 rows each: token x query head of the group) of one KV head of a chunk.
 struct FullArgs {
     // partial records (O unnormalised, m in log2 units, l): one row per (token, query head) for an item's first piece, then
@@ -28,9 +29,13 @@ struct FullArgs {
     int num_seqs;
     int64_t own_row;           // first row of the own blocks' records
     bool prefix;         // shared prefixes: every item leaves records
+    bool tree = false;   // draft trees
+    int mask_words = 0;  // 64-bit words of a token's mask
+    const uint64_t* tree_mask = nullptr;  // [tokens][mask_words]; none: each run is a chain
+    const void* v_cache = nullptr;        // draft trees
 };
 
-size_t paged_full_smem_bytes(int narrow);
+size_t paged_full_smem_bytes(int narrow, bool tree = false);
 cudaError_t launch_paged_full(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const PrefillArgs& a, const FullArgs& f, int narrow, int grid, bool prepared,
                               cudaStream_t stream);
