@@ -385,6 +385,9 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 before += bu;
                 items_at += bc;
             }
+            // TREE: rounds only where the items are twice the KV heads of the runs or more, that is, where most keys are read by
+            // several items
+            const bool shared_keys = TREE && M >= 2 * n_chunks * a.Hkv;
             int share = 0x7fffffff;
             if (T > kMostUnits) {  // nothing is done
                 T = 0;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
             } else {
                 share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
             }
-            if (!f.prefix && M >= 2 * ncta && T / M >= kRoundUnits) rounds = min(kRounds, M / ncta - 1);
+            if ((TREE ? shared_keys : !f.prefix) && M >= 2 * ncta && T / M >= kRoundUnits) rounds = min(kRounds, M / ncta - 1);
             if (tid == 0) {
                 mine[5] = mine[12] = rounds;
                 mine[6] = 0;
@@ -849,7 +852,6 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 const bool valid = row < it.tokens * a.G;
                 const bool live = (row & ~31) < it.tokens * a.G;  // some row of this warp is the item's
                 const int h = it.head_pair & 0xffff;
-                const int2 run = TREE ? own[i] : make_int2(0, 0);
                 const size_t tok_row = (static_cast<size_t>(it.q_row) + (row >> g_shift)) * a.Hq + (static_cast<size_t>(h) << g_shift) +
                                        (row & (a.G - 1));
                 float m_ref = kLowest, l_run = 0.f;
@@ -865,6 +867,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 // keys past the last are -inf, and -inf times zero is no number)
                 if (sm_log2 == 0.f) sm_log2 = 1.17549435e-38f;
                 int left = it.keys - (it.j0 + j_first) * kKeys;  // keys from the current tile on
+                // tiles with that many or more hold none of the run's own keys (TREE), none past the last
+                const int own_left = TREE ? it.keys - own[i].y + kKeys : kKeys;
 #pragma unroll 1
                 for (int j = j_first; j < tiles; j += step, left -= step * kKeys, ++c) {
                     const int b = c & 1;
@@ -880,9 +884,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         float v[64];
                         tmem_ld64(tS, v);
                         if constexpr (TREE) {
-                            const int base = it.keys - left;
-                            if (base + kKeys > run.y) {  // keys that are not seen: their probabilities come out as 0
-                                const uint64_t see = visible(f, run, it.q_row + min(row >> g_shift, it.tokens - 1), base, it.keys);
+                            if (left < own_left) {  // keys that are not seen: their probabilities come out as 0
+                                const uint64_t see = visible(f, own[i], it.q_row + min(row >> g_shift, it.tokens - 1), it.keys - left, it.keys);
                                 const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
                                 for (int u = 0; u < 64; ++u) v[u] = (u < 32 ? lo >> u : hi >> (u - 32)) & 1u ? v[u] : -INFINITY;
@@ -945,14 +948,14 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         }
                     }
                     // V rows past the last key: zero, once they have landed
-                    if (NARROW != 2 && (TREE ? it.keys - left + kKeys > run.y : left < kKeys) && (TREE || t == 0 || !pair)) {
+                    if (NARROW != 2 && left < own_left && (TREE || t == 0 || !pair)) {
                         if (!warp_wait(bar + 8 * (kFVThere + t), zeroed++ & 1, a.timeout_ns)) {
                             give_up();
                             break;
                         }
                         const int st = mine[8 + t];
                         constexpr int kRowChunks = NARROW == 1 ? 8 : 16;  // 16-byte pieces of a key's row
-                        const int from = TREE ? max(0, run.y - (it.keys - left)) : left;  // the first row to look at
+                        const int from = TREE ? max(0, own[i].y - (it.keys - left)) : left;  // the first row to look at
 #pragma unroll 1
                         for (int u = r; u < (kKeys - from) * kRowChunks; u += 128) {
                             const int key = from + u / kRowChunks, k = u % kRowChunks;
@@ -1051,7 +1054,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     }
                     if (rec && valid) f.rec_ml[rec_row] = make_float2(m_ref, l_run);
                     if (TREE && NARROW != 2 && valid && mine[13])
-                        add_odd<NARROW>(a, f, it, run, it.q_row + (row >> g_shift), h, rec ? rec_o : nullptr,
+                        add_odd<NARROW>(a, f, it, own[i], it.q_row + (row >> g_shift), h, rec ? rec_o : nullptr,
                                         reinterpret_cast<__nv_bfloat16*>(out_o));
                 }
                 tc_fence_before();  // the next item's first P V overwrites O, once this group's P of it is there
