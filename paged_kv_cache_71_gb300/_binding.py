@@ -472,25 +472,19 @@ def pkv_paged_cross_attention(out, q, cu_q, kv_lens, k_cache, v_cache, cache: Ca
         _check(status, "pkv_paged_cross_attention")
 
 
-def _rows(t, dtype, heads: int, D: int, tokens: int, device: int) -> bool:
-    """[tokens][heads][D] whose tokens may be further apart than a token is long (parts of a fused projection's rows)."""
-    return (t.dtype is dtype and t.shape == (tokens, heads, D) and t.get_device() == device
-            and (tokens < 2 or t.stride(0) >= heads * D) and t.stride(2) == 1 and (heads == 1 or t.stride(1) == D))
-
-
 def _refuse_rows(func: str, name: str, t, dtypes, shape) -> None:
     if t.dtype not in dtypes:
         raise PkvError(1, func, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.shape != shape:
         raise PkvError(1, func, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.numel() and not ((shape[0] < 2 or t.stride(0) >= shape[1] * shape[2]) and t.stride(2) == 1
-                          and (shape[1] == 1 or t.stride(1) == shape[2])):
+    if t.numel() and not _apart(t.stride(), shape):
         raise PkvError(1, func, f"{name} must have contiguous, separate tokens (strides {t.stride()})")
 
 
-def _token_stride(t, width: int) -> int:
-    """Elements from token to token (a single token's stride may be anything)."""
-    return t.stride(0) if t.shape[0] > 1 else width
+def _apart(strides, shape) -> bool:
+    """[tokens][heads][D] whose tokens may be further apart than a token is long (parts of a fused projection's rows)."""
+    tokens, heads, D = shape
+    return strides[2] == 1 and (strides[1] == D or heads == 1) and (tokens < 2 or strides[0] >= heads * D)
 
 
 def pkv_rope_and_cache(q_out, q, k_new, v_new, positions, slot_mapping, inv_freq, k_cache, v_cache, cache: CacheDesc,
@@ -499,42 +493,53 @@ def pkv_rope_and_cache(q_out, q, k_new, v_new, positions, slot_mapping, inv_freq
     inv_freq: fp32, one per pair of rotated elements (rotary_frequencies makes it).  q and q_out None: keys and values only;
     k_new and v_new None: queries only."""
     func, L, dev, D = "pkv_rope_and_cache", lib(), _here(positions), cache.head_dim
-    if positions.dim() != 1 or inv_freq.dim() != 1:
-        _dims(func, positions=(positions, 1), inv_freq=(inv_freq, 1))
-    n, hkv, caches = positions.shape[0], cache.num_kv_heads, (cache.num_blocks, cache.block_size, cache.num_kv_heads, D)
     some = q if q is not None else k_new
     if some is None or (q is None) != (q_out is None) or (k_new is None) != (v_new is None):
         raise PkvError(1, func, "q comes with q_out, k_new with v_new, and one of the pairs is needed")
-    if q is not None and q.dim() != 3:
-        _dims(func, q=(q, 3))
-    src, heads = some.dtype, 0 if q is None else q.shape[1]
-    if not (src in _FLOATS and _fits(positions, torch.int32, (n,), dev) and _fits(inv_freq, torch.float32, inv_freq.shape, dev)
-            and _word(device_error, dev) and (slot_mapping is None or _fits(slot_mapping, torch.int64, (n,), dev))
-            and (q is None or (_rows(q, src, heads, D, n, dev) and _rows(q_out, src, heads, D, n, dev)))
-            and (k_new is None or (_rows(k_new, src, hkv, D, n, dev) and _rows(v_new, src, hkv, D, n, dev)
-                                   and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and slot_mapping is not None
-                                   and _fits(k_cache, v_cache.dtype, caches, dev) and _fits(v_cache, k_cache.dtype, caches, dev)))):
+    if positions.dim() != 1 or inv_freq.dim() != 1 or some.dim() != 3:
+        _dims(func, positions=(positions, 1), inv_freq=(inv_freq, 1), **{"k_new" if q is None else "q": (some, 3)})
+    src, i32, f32 = some.dtype, torch.int32, torch.float32
+    n, hkv, pairs = positions.shape[0], cache.num_kv_heads, inv_freq.shape[0]
+    heads = 0 if q is None else q.shape[1]
+    good = (src in _FLOATS and positions.dtype is i32 and inv_freq.dtype is f32 and positions.is_contiguous()
+            and inv_freq.is_contiguous() and inv_freq.get_device() == dev and _word(device_error, dev)
+            and (slot_mapping is None or _fits(slot_mapping, torch.int64, (n,), dev)))
+    q_stride = q_out_stride = k_stride = v_stride = 0
+    kc = vc = None
+    if good and q is not None:
+        shape, s0, s1 = (n, heads, D), q.stride(), q_out.stride()
+        good = (q_out.dtype is src and q.shape == shape == q_out.shape and _apart(s0, shape) and (s1 == s0 or _apart(s1, shape))
+                and q.get_device() == dev == q_out.get_device())
+        q_stride, q_out_stride = (s0[0], s1[0]) if n > 1 else (heads * D, heads * D)  # (a single token's stride may be anything)
+    if good and k_new is not None:
+        shape, s0, s1, caches = (n, hkv, D), k_new.stride(), v_new.stride(), (cache.num_blocks, cache.block_size, hkv, D)
+        kind = k_cache.dtype
+        good = (slot_mapping is not None and k_new.dtype is src is v_new.dtype and k_new.shape == shape == v_new.shape
+                and _apart(s0, shape) and (s1 == s0 or _apart(s1, shape)) and _DTYPE_CODE.get(kind) == cache.dtype
+                and v_cache.dtype is kind and k_cache.shape == caches == v_cache.shape and k_cache.is_contiguous()
+                and v_cache.is_contiguous()
+                and k_new.get_device() == dev == v_new.get_device() == k_cache.get_device() == v_cache.get_device())
+        k_stride, v_stride = (s0[0], s1[0]) if n > 1 else (hkv * D, hkv * D)
+        kc, vc = k_cache.data_ptr(), v_cache.data_ptr()
+    if not good:
         if k_new is not None and slot_mapping is None:
             raise PkvError(1, func, "k_new and v_new need slot_mapping")
         for name, t, h in (("q", q, heads), ("q_out", q_out, heads), ("k_new", k_new, hkv), ("v_new", v_new, hkv)):
             if t is not None:
                 _refuse_rows(func, name, t, _FLOATS if t is some else (src,), (n, h, D))
+        caches = (cache.num_blocks, cache.block_size, hkv, D)
         pools = {} if k_new is None else dict(k_cache=(k_cache, _cache_dtypes(cache), caches), v_cache=(v_cache, (k_cache.dtype,), caches))
         _refuse(func, _device(), device_error, positions=(positions, _I32, (n,)), slot_mapping=(slot_mapping, _I64, (n,)),
-                inv_freq=(inv_freq, (torch.float32,), inv_freq.shape), **pools)
+                inv_freq=(inv_freq, (f32,), (pairs,)), **pools)
         for name, t in (("q", q), ("q_out", q_out), ("k_new", k_new), ("v_new", v_new)):
             if t is not None and t.get_device() != _device():
                 raise PkvError(1, func, f"{name} is on {t.device}, not on the current CUDA device")
     if n == 0:
         return
-    qw, kw = heads * D, hkv * D
-    q_stride, q_out_stride = (0, 0) if q is None else (_token_stride(q, qw), _token_stride(q_out, qw))
-    k_stride, v_stride = (0, 0) if k_new is None else (_token_stride(k_new, kw), _token_stride(v_new, kw))
-    kc, vc = (None, None) if k_new is None else (k_cache.data_ptr(), v_cache.data_ptr())
     status = L.pkv_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k_new), _ptr(v_new), _DTYPE_CODE[src], q_out_stride, q_stride, k_stride,
-                                  v_stride, positions.data_ptr(), _ptr(slot_mapping), n, heads, inv_freq.data_ptr(),
-                                  2 * inv_freq.shape[0], int(interleaved), float(rope_scale), kc, vc, ctypes.byref(cache),
-                                  _ptr(device_error), _stream(stream, dev))
+                                  v_stride, positions.data_ptr(), _ptr(slot_mapping), n, heads, inv_freq.data_ptr(), 2 * pairs,
+                                  1 if interleaved else 0, float(rope_scale), kc, vc, ctypes.byref(cache), _ptr(device_error),
+                                  _stream(stream, dev))
     if status:
         _check(status, func)
 

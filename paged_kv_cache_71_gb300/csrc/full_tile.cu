@@ -780,26 +780,34 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
 #pragma unroll 1
                     for (; g < end && ok; ++g) {
                         const int slot = g % kSlots, st = g % kStages;
-                        ok = warp_wait(bar + 8 * (kFStg + 4 * is_v + slot), (g / kSlots) & 1, a.timeout_ns) &&
-                             (g < kStages || warp_wait(bar + 8 * (empty + st), (g / kStages - 1) & 1, a.timeout_ns));
+                        // the codes have landed (even lanes wait), their place in the ring is free (odd lanes)
+                        ok = ((lane & 1) && g < kStages) ||
+                             mbar_wait_bounded(bar + 8 * (lane & 1 ? empty + st : kFStg + 4 * is_v + slot),
+                                               (lane & 1 ? g / kStages - 1 : g / kSlots) & 1, a.timeout_ns);
+                        ok = __all_sync(kFull, ok);
                         if (!ok) break;
                         const uint8_t* src = smem + PL::kOffStg + (is_v * PL::kSlots + slot) * kStgSlot + r * 128;
                         uint8_t* dst = smem + (is_v ? PL::kOffV : PL::kOffK) + st * kStage + r * 128;
-#pragma unroll 4
-                        for (int k = 0; k < 8; ++k) {  // 16 codes: head dims 16 k .. 16 k + 15
-                            const uint4 wv = *reinterpret_cast<const uint4*>(src + ((k ^ sw) * 16));
-                            const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
-                            uint32_t o[8];
+                        // four pieces of 16 codes at a time, their loads before the stores (which the compiler may not pass)
+#pragma unroll 1
+                        for (int q = 0; q < 8; q += 4) {
+                            uint4 in[4];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const uint32_t fl = ws[u] ^ 0x80808080u;
-                                o[2 * u] = s8x2_to_f16x2(fl, 0);
-                                o[2 * u + 1] = s8x2_to_f16x2(fl, 2);
+                            for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(src + (((q + k) ^ sw) * 16));
+                            uint8_t* dh = dst + (q >> 2) * kKvHalf;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {  // head dims 16 (q + k) .. 16 (q + k) + 15
+                                const uint32_t ws[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+                                uint32_t o[8];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const uint32_t fl = ws[u] ^ 0x80808080u;
+                                    o[2 * u] = s8x2_to_f16x2(fl, 0);
+                                    o[2 * u + 1] = s8x2_to_f16x2(fl, 2);
+                                }
+                                *reinterpret_cast<uint4*>(dh + (((2 * k) ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+                                *reinterpret_cast<uint4*>(dh + (((2 * k + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                             }
-                            uint8_t* dh = dst + (k >> 2) * kKvHalf;
-                            const int lc = 2 * (k & 3);
-                            *reinterpret_cast<uint4*>(dh + ((lc ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(dh + (((lc + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         fence_proxy_async_smem();  // the MMA (async proxy) reads what was written; the next copy overwrites
                         __syncwarp();

@@ -10,9 +10,10 @@
 // p * phase mod 2^64 is the reduced angle, off by at most |p| 2^-63 turns.  Its upper 32 bits (2^-32 turns) go to
 // sincospi.  Every (token, pair) is computed once for all heads of a CTA, through shared memory.
 //
-// Bound by HBM (large calls) or launch latency.  A thread's unit is 8 elements of one head, two groups of four (of the
-// first and the second half of the pairs, or eight neighbours), 16 threads to a head of 128: loads and stores of a warp cover
-// whole 32-byte sectors in either pairing, and the rotated part may be any multiple of 8.
+// Bound by HBM (large calls) or launch latency.  A thread's unit is two 16-byte groups of one head's elements, of the first and
+// the second half of the pairs or one behind the other (two 8-byte groups of bf16 where the rotated part is no multiple of
+// 16): a warp's loads and stores cover whole 128-byte lines.  A thread has all of its units (up to four) on their way before
+// the angles are computed, whose loads, sines and barrier they cover.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -22,8 +23,8 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;      // units of a thread in flight
-constexpr int kMaxTokens = 4;  // tokens of a CTA
+constexpr int kUnits = 4;      // most units of a thread
+constexpr int kMaxTokens = 4;  // most tokens of a CTA
 
 // f turns per radian times 2^64, mod 2^64, for a finite f: the mantissa times floor(2^64 / (2 pi)), shifted by the exponent.
 // (Frequencies of 2^24 and more, far beyond the one radian per position that models use, lose bits.)
@@ -41,48 +42,109 @@ __device__ __forceinline__ uint64_t turns(float f) {
     return u >> 31 ? 0 - t : t;
 }
 
-template <int T>
-__device__ __forceinline__ float4 load4(const uint8_t* base, int64_t elem) {
-    if constexpr (T == PKV_F32) return *reinterpret_cast<const float4*>(base + elem * 4);
-    const uint2 w = *reinterpret_cast<const uint2*>(base + elem * 2);
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-template <int T>
-__device__ __forceinline__ void store4(uint8_t* base, int64_t elem, float4 x, float scale) {
-    if constexpr (T == PKV_F32) {
-        *reinterpret_cast<float4*>(base + elem * 4) = x;
-    } else if constexpr (T == PKV_BF16) {
-        const uint32_t a = float_to_bf16_bits(x.x) | static_cast<uint32_t>(float_to_bf16_bits(x.y)) << 16;
-        const uint32_t b = float_to_bf16_bits(x.z) | static_cast<uint32_t>(float_to_bf16_bits(x.w)) << 16;
-        *reinterpret_cast<uint2*>(base + elem * 2) = make_uint2(a, b);
-    } else {  // the cache write's conversions: an IEEE division, then round to nearest even, saturated
-        const float y[4] = {x.x / scale, x.y / scale, x.z / scale, x.w / scale};
-        uint32_t w = 0;
+// V elements of type T as they lie in memory: 16 bytes, or 8
+template <int T, int V>
+struct Group {
+    static constexpr int kWords = V * (T == PKV_F32 ? 4 : 2) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const uint8_t* base, int64_t elem) {
+        const uint8_t* p = base + elem * (T == PKV_F32 ? 4 : 2);
+        if constexpr (kWords == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x, w[1] = x.y;
+        }
+    }
+    __device__ __forceinline__ void values(float (&f)[V]) const {
+        if constexpr (T == PKV_F32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w |= static_cast<uint32_t>(T == PKV_INT8 ? float_to_s8_sym(y[i]) : float_to_e4m3_sat(y[i])) << (8 * i);
-        *reinterpret_cast<uint32_t*>(base + elem) = w;
+            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 x = bf16x2_to_float2(w[i]);
+                f[2 * i] = x.x;
+                f[2 * i + 1] = x.y;
+            }
+        }
+    }
+};
+
+template <int T, int V>
+__device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const float (&f)[V], float scale) {
+    constexpr int kBytes = T == PKV_F32 ? 4 : T == PKV_BF16 ? 2 : 1, kWords = V * kBytes / 4;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if constexpr (T == PKV_F32) {
+            w[i] = __float_as_uint(f[i]);
+        } else if constexpr (T == PKV_BF16) {
+            w[i] = float_to_bf16_bits(f[2 * i]) | static_cast<uint32_t>(float_to_bf16_bits(f[2 * i + 1])) << 16;
+        } else {  // the cache write's conversions: an IEEE division, then round to nearest even, saturated
+            w[i] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float y = f[4 * i + k] / scale;
+                w[i] |= static_cast<uint32_t>(T == PKV_INT8 ? float_to_s8_sym(y) : float_to_e4m3_sat(y)) << (8 * k);
+            }
+        }
+    }
+    uint8_t* p = base + elem * kBytes;
+    if constexpr (kWords == 8) {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if constexpr (kWords == 4) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (kWords == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
     }
 }
 
 }  // namespace
 
-// Grid: x runs of `per_cta` tokens, y parts of the heads (queries, keys and values in a row).
-template <int SRC, int DST>
+// Grid: x runs of `per_cta` tokens, y parts of the heads (queries, keys and values in a row).  V: elements of a group.
+template <int SRC, int DST, int V>
 __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, int per_cta) {
-    __shared__ __align__(16) float2 turn[kMaxTokens * 64];  // cos, sin of each token's pairs
+    // cos, sin of each token's pairs, two pairs to 16 bytes; those that the threads of a head read at a time side by side
+    __shared__ float4 turn[kMaxTokens][32];
     __shared__ int64_t slot_of[kMaxTokens];  // -1: nothing of the token is written
+    constexpr int kQuads = V / 2;            // 16-byte pieces of `turn` that a unit needs
+    constexpr int kPlaces = 32 / kQuads;     // units of a head of 128
     const int tid = threadIdx.x, t0 = blockIdx.x * per_cta, n = min(per_cta, a.tokens - t0);
-    const int half = a.rot >> 1;
-    if (tid < n) {
-        int64_t s = a.slots ? a.slots[t0 + tid] : 0;
+    const int half = a.rot >> 1, u_shift = a.d_shift - (V == 8 ? 4 : 3);
+    const int u = tid & ((1 << u_shift) - 1);  // this thread's unit of its heads
+    const int heads = a.Hq + 2 * a.Hkv, part = (heads + gridDim.y - 1) / gridDim.y;
+    const int h0 = blockIdx.y * part, nh = min(part, heads - h0), rows = n * nh;
+    if (nh <= 0) return;
+    const bool turned = 2 * V * u < a.rot;
+    const int first = turned && !a.interleaved ? V * u : 2 * V * u, second = turned && !a.interleaved ? half + V * u : first + V;
+    const int row0 = tid >> u_shift, step = kThreads >> u_shift;
+    auto token_of = [&](int row) { return (row >= nh) + (row >= 2 * nh) + (row >= 3 * nh); };
+    Group<SRC, V> x[kUnits], y[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+        const int row = row0 + k * step;
+        if (row >= rows) break;
+        const int t = token_of(row), h = h0 + row - t * nh;
+        const bool is_q = h < a.Hq, is_k = h < a.Hq + a.Hkv;
+        const uint8_t* src = is_q ? a.q : is_k ? a.k : a.v;
+        const int64_t at = (t0 + t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) +
+                           (static_cast<int64_t>(h - (is_q ? 0 : is_k ? a.Hq : a.Hq + a.Hkv)) << a.d_shift);
+        x[k].load(src, at + first);
+        y[k].load(src, at + second);
+    }
+    if (tid >= kThreads - n) {  // (the last threads: the first ones have the angles)
+        const int t = kThreads - 1 - tid;
+        int64_t s = a.slots ? a.slots[t0 + t] : 0;
         if (s >= a.pool_slots) {
             if (blockIdx.y == 0) raise_error(a.err, PKV_DEVERR_BAD_SLOT);
             s = -1;
         }
-        slot_of[tid] = s;
+        slot_of[t] = s;
     }
     for (int i = tid; i < n * half; i += kThreads) {
         const int t = i / half, p = i - t * half;
@@ -91,99 +153,82 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
         float s, c;
         sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
         if (!(fabsf(f) <= 3.402823466e38f)) c = s = __int_as_float(0x7fc00000);
-        turn[t * 64 + p] = make_float2(c * a.factor, s * a.factor);
+        const int quad = p >> 1;
+        reinterpret_cast<float2*>(&turn[t][(quad % kQuads) * kPlaces + quad / kQuads])[p & 1] = make_float2(c * a.factor, s * a.factor);
     }
     __syncthreads();
-    const int u_shift = a.d_shift - 3, u = tid & ((1 << u_shift) - 1);  // this thread's unit of its heads
-    const int step = kThreads >> u_shift, heads = a.Hq + 2 * a.Hkv;
-    const int part = (heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * part, nh = min(part, heads - h0);
-    if (nh <= 0) return;
-    const bool turned = 8 * u < a.rot;
-    const int first = turned && !a.interleaved ? 4 * u : 8 * u, second = turned && !a.interleaved ? half + 4 * u : 8 * u + 4;
-    int t = 0, h = tid >> u_shift;
-    while (true) {
-        while (h >= nh && t < n) {
-            h -= nh;
-            ++t;
-        }
-        if (t >= n) break;
-        float4 x[kUnits], y[kUnits];
-        int tok[kUnits], head[kUnits];
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            while (h >= nh && t < n) {
-                h -= nh;
-                ++t;
-            }
-            tok[k] = t;
-            head[k] = h0 + h;
-            if (t < n && slot_of[t] >= 0) {
-                const bool is_q = head[k] < a.Hq, is_k = head[k] < a.Hq + a.Hkv;
-                const uint8_t* src = is_q ? a.q : is_k ? a.k : a.v;
-                const int64_t at = (t0 + t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) +
-                                   (static_cast<int64_t>(head[k] - (is_q ? 0 : is_k ? a.Hq : a.Hq + a.Hkv)) << a.d_shift);
-                x[k] = load4<SRC>(src, at + first);
-                y[k] = load4<SRC>(src, at + second);
-            } else {
-                tok[k] = -1;
-            }
-            h += step;
-        }
+    for (int k = 0; k < kUnits; ++k) {
+        const int row = row0 + k * step;
+        if (row >= rows) break;
+        const int t = token_of(row), h = h0 + row - t * nh;
+        const int64_t slot = slot_of[t];
+        if (slot < 0) continue;
+        const bool is_q = h < a.Hq, is_k = h < a.Hq + a.Hkv;
+        float p[V], q[V];
+        x[k].values(p);
+        y[k].values(q);
+        if (turned && is_k) {
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            if (tok[k] < 0) continue;
-            const bool is_q = head[k] < a.Hq, is_k = head[k] < a.Hq + a.Hkv;
-            if (turned && is_k) {
-                const float4* cs = reinterpret_cast<const float4*>(&turn[tok[k] * 64 + 4 * u]);
-                const float4 c0 = cs[0], c1 = cs[1];  // cos, sin of pairs 4 u .. 4 u + 3
-                const float4 p = x[k], q = y[k];
-                if (a.interleaved) {
-                    x[k] = make_float4(p.x * c0.x - p.y * c0.y, p.y * c0.x + p.x * c0.y, p.z * c0.z - p.w * c0.w, p.w * c0.z + p.z * c0.w);
-                    y[k] = make_float4(q.x * c1.x - q.y * c1.y, q.y * c1.x + q.x * c1.y, q.z * c1.z - q.w * c1.w, q.w * c1.z + q.z * c1.w);
-                } else {
-                    x[k] = make_float4(p.x * c0.x - q.x * c0.y, p.y * c0.z - q.y * c0.w, p.z * c1.x - q.z * c1.y, p.w * c1.z - q.w * c1.w);
-                    y[k] = make_float4(q.x * c0.x + p.x * c0.y, q.y * c0.z + p.y * c0.w, q.z * c1.x + p.z * c1.y, q.w * c1.z + p.w * c1.w);
+            for (int i = 0; i < kQuads; ++i) {
+                const float4 cs = turn[t][i * kPlaces + u];  // pairs V u + 2 i and the next
+                const float c[2] = {cs.x, cs.z}, s[2] = {cs.y, cs.w};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float *l, *r;  // the pair
+                    if (a.interleaved) {
+                        l = i < kQuads / 2 ? &p[4 * i + 2 * e] : &q[4 * (i - kQuads / 2) + 2 * e];
+                        r = l + 1;
+                    } else {
+                        l = &p[2 * i + e];
+                        r = &q[2 * i + e];
+                    }
+                    const float lv = *l, rv = *r;
+                    *l = lv * c[e] - rv * s[e];
+                    *r = rv * c[e] + lv * s[e];
                 }
             }
-            if (is_q) {
-                const int64_t at = (t0 + tok[k]) * a.q_out_stride + (static_cast<int64_t>(head[k]) << a.d_shift);
-                store4<SRC>(a.q_out, at + first, x[k], 1.f);
-                store4<SRC>(a.q_out, at + second, y[k], 1.f);
-            } else {
-                const int kv = head[k] - (is_k ? a.Hq : a.Hq + a.Hkv);
-                uint8_t* dst = is_k ? a.k_cache : a.v_cache;
-                const float* hs = is_k ? a.k_head : a.v_head;
-                const float scale = hs ? __ldg(hs + kv) : is_k ? a.k_scale : a.v_scale;
-                const int64_t at = (slot_of[tok[k]] * a.Hkv + kv) << a.d_shift;
-                store4<DST>(dst, at + first, x[k], scale);
-                store4<DST>(dst, at + second, y[k], scale);
-            }
+        }
+        if (is_q) {
+            const int64_t at = (t0 + t) * a.q_out_stride + (static_cast<int64_t>(h) << a.d_shift);
+            store_group<SRC, V>(a.q_out, at + first, p, 1.f);
+            store_group<SRC, V>(a.q_out, at + second, q, 1.f);
+        } else {
+            const int kv = h - (is_k ? a.Hq : a.Hq + a.Hkv);
+            uint8_t* dst = is_k ? a.k_cache : a.v_cache;
+            const float* hs = is_k ? a.k_head : a.v_head;
+            const float scale = hs ? __ldg(hs + kv) : is_k ? a.k_scale : a.v_scale;
+            const int64_t at = (slot * a.Hkv + kv) << a.d_shift;
+            store_group<DST, V>(dst, at + first, p, scale);
+            store_group<DST, V>(dst, at + second, q, scale);
         }
     }
 }
 
 cudaError_t launch_rope_and_cache(const RopeArgs& a, int src_dtype, int dst_dtype, int sms, cudaStream_t stream) {
-    const int heads = a.Hq + 2 * a.Hkv, at_once = kThreads >> (a.d_shift - 3);
-    // one token per CTA until every SM has its fill of CTAs; below that, parts of a token's heads
-    const int fill = sms * (2048 / kThreads);
-    const int per_cta = std::min(kMaxTokens, std::max(1, a.tokens / fill));
+    // bf16 groups of 16 bytes need whole units in the rotated part
+    const int V = src_dtype == PKV_BF16 && a.rot % 16 == 0 ? 8 : 4;
+    const int units = (a.Hq + 2 * a.Hkv) << (a.d_shift - (V == 8 ? 4 : 3));  // of a token
+    // as many tokens as four units a thread hold, or parts of a token; one unit a thread while that leaves SMs without a CTA
+    int per_cta = std::max(1, std::min({kMaxTokens, kThreads * kUnits / units, (a.tokens + sms - 1) / sms}));
     const int runs = (a.tokens + per_cta - 1) / per_cta;
-    const int parts = std::max(1, std::min((heads + at_once - 1) / at_once, fill / runs));
+    int parts = (units + kThreads * kUnits - 1) / (kThreads * kUnits);
+    if (per_cta == 1 && static_cast<int64_t>(runs) * parts < 2 * sms) parts = (units + kThreads - 1) / kThreads;
+    const int heads = a.Hq + 2 * a.Hkv, at_once = kThreads / (units / heads);  // (a part is whole heads)
+    parts = std::max(parts, (heads + at_once * kUnits - 1) / (at_once * kUnits));
     const dim3 grid(runs, parts);
-#define PKV_ROPE(S_, D_)                                                              \
-    if (src_dtype == S_ && dst_dtype == D_) {                                         \
-        rope_and_cache_kernel<S_, D_><<<grid, kThreads, 0, stream>>>(a, per_cta);     \
-        return cudaGetLastError();                                                    \
+#define PKV_ROPE_V(S_, D_, V_)                                                            \
+    if (src_dtype == S_ && dst_dtype == D_ && V == V_) {                                  \
+        rope_and_cache_kernel<S_, D_, V_><<<grid, kThreads, 0, stream>>>(a, per_cta);     \
+        return cudaGetLastError();                                                        \
     }
-    PKV_ROPE(PKV_F32, PKV_F32)
-    PKV_ROPE(PKV_F32, PKV_BF16)
-    PKV_ROPE(PKV_F32, PKV_FP8_E4M3)
-    PKV_ROPE(PKV_F32, PKV_INT8)
-    PKV_ROPE(PKV_BF16, PKV_F32)
-    PKV_ROPE(PKV_BF16, PKV_BF16)
-    PKV_ROPE(PKV_BF16, PKV_FP8_E4M3)
-    PKV_ROPE(PKV_BF16, PKV_INT8)
+#define PKV_ROPE(D_) PKV_ROPE_V(PKV_F32, D_, 4) PKV_ROPE_V(PKV_BF16, D_, 8) PKV_ROPE_V(PKV_BF16, D_, 4)
+    PKV_ROPE(PKV_F32)
+    PKV_ROPE(PKV_BF16)
+    PKV_ROPE(PKV_FP8_E4M3)
+    PKV_ROPE(PKV_INT8)
 #undef PKV_ROPE
+#undef PKV_ROPE_V
     return cudaErrorInvalidValue;
 }
 
