@@ -1191,12 +1191,12 @@ static pkv_status check_full(const char* what, int32_t q_dtype, const pkv_cache_
 static pkv_status full_setup(PrefillArgs* out_a, CUtensorMap* qm, CUtensorMap* km, CUtensorMap* vm, void* out, const void* q,
                              const void* k_cache, const void* v_cache, const pkv_cache_desc& c, int tokens, int Hq,
                              const int32_t* cu, const int32_t* kv_lens, int chunks, const int32_t* tables, int MB,
-                             float scale, int32_t* err) {
+                             float scale, int32_t* err, bool tree = false) {
     const int Hkv = c.num_kv_heads, S = c.block_size, G = Hq / Hkv;
     const bool nar = narrow(c.dtype);
     const float kLog2e = 1.4426950408889634f;
     // units of the whole stream, at most: the kernel counts them in 32 bits
-    const int64_t units = 2 * ((static_cast<int64_t>(MB) * S + 63) / 64) + 32;
+    const int64_t units = (tree ? 10 : 2) * ((static_cast<int64_t>(MB) * S + 63) / 64) + (tree ? 35 : 32);
     if ((static_cast<int64_t>(tokens) / (2 * (128 / G)) + chunks) * Hkv * units > INT32_MAX - 4096)
         return fail(PKV_ERR_OUT_OF_RANGE, "query tiles * num_kv_heads * key tiles must stay below 2^31");
     PrefillArgs a;
@@ -1465,7 +1465,7 @@ static pkv_status stream_entry(const char* what, void* out, const void* q, int32
     PrefillArgs pa;
     CUtensorMap qm, km, vm;
     if ((st = full_setup(&pa, &qm, &km, &vm, out, nk ? q_ops : q, k_cache, v_cache, *cache, total_q_tokens, num_q_heads, cu_q, kv_lens,
-                         num_seqs, block_tables, max_blocks_per_seq, scale, device_error)) != PKV_OK)
+                         num_seqs, block_tables, max_blocks_per_seq, scale, device_error, tree)) != PKV_OK)
         return st;
     FullArgs fa = full_args(fs, workspace, nullptr, 0);
     fa.tree = tree;

@@ -50,6 +50,19 @@ constexpr int kMinShare = 8;
 // What an item costs beside its key tiles, which count w units each (w: query tiles).  4 units for either kind, tried first,
 // left the SMs with many short items of two query tiles behind: 12 prompts over long states took 810 us against 785.
 __device__ constexpr int item_units(int w) { return 4 * w; }
+// Draft trees (TREE): units of about 220 cycles, from the CTAs' cycles over 96 ragged trees (least squares: a key tile of one
+// query tile 1070 bf16, 1137 FP8, 1485 INT8, of two 1708, 2205, 2118, an item 4986, 7817, 6269).  Runs differ in their rows from
+// sequence to sequence, so that items of one and of two query tiles share the stream: with the units above the slowest SM took
+// 1.2 to 1.3 times the mean.  (Cuts may then fall inside a key tile, which goes to the later share whole.)
+template <int NARROW, bool TREE>
+struct Cost {
+    static constexpr int kItem = NARROW == 1 ? 35 : 30, kPair = 10, kSingle = NARROW == 1 ? 5 : 7;
+    static constexpr int kLeast = TREE ? kItem + kPair : kMinShare;  // fewest units in a share: an item's and a key tile's
+    __device__ static constexpr int item(int w) { return TREE ? kItem : item_units(w); }
+    __device__ static constexpr int tile(int w) { return TREE ? (w == 1 ? kSingle : kPair) : w; }
+    __device__ static int tiles(int units, int w) { return TREE ? (w == 1 ? units / kSingle : units / kPair) : units >> (w - 1); }
+    __device__ static int up(int units) { return TREE ? units : (units + 1) & ~1; }
+};
 constexpr int kBatch = 128;    // items that a CTA lists at a time
 constexpr int kEmpty = 512;    // chunks without keys that it lists
 // Cross attention, at least two items for every CTA, and long ones: the items, ordered by KV head, are first handed out whole,
@@ -236,6 +249,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     const int g_shift = 31 - __clz(a.G);  // G divides 128
     const int rows_q = kRows >> g_shift, cta_q = 2 * rows_q, cta_shift = 8 - g_shift;
     const int n_chunks = a.nseq;
+    using C = Cost<NARROW, TREE>;
 
     if (tid < kFBars) {
         const int i = tid;
@@ -276,7 +290,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         k.table = (f.prefix ? k.q0 : c) * a.MB;
         k.w = k.tokens > rows_q ? 2 : 1;
         k.kt = (max(k.keys, 0) + kKeys - 1) / kKeys;
-        k.ku = k.kt > 0 ? (k.kt * k.w + item_units(k.w) + 1) & ~1 : 0;
+        k.ku = k.kt > 0 ? C::up(k.kt * C::tile(k.w) + C::item(k.w)) : 0;
         k.items = k.kt > 0 ? ((k.tokens + cta_q - 1) >> cta_shift) * a.Hkv : 0;
         return k;
     };
@@ -284,23 +298,24 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     auto put_item = [&](int slot, const Chunk& k, int start, int m, int x0, int x1, int rounds, bool first) {
         const int n_tiles = (k.tokens + cta_q - 1) >> cta_shift;
         const int tile = rounds ? m % n_tiles : m / a.Hkv, h = rounds ? m / n_tiles : m - tile * a.Hkv, t0 = tile << cta_shift;
-        const int Uk = start + m * k.ku, j0 = max(0, x0 - Uk - item_units(k.w)) >> (k.w - 1);
+        const int Uk = start + m * k.ku, j0 = C::tiles(max(0, x0 - Uk - C::item(k.w)), k.w);
         Item it;
         it.q_row = k.q0 + t0;
         it.tokens = min(cta_q, k.tokens - t0);
         it.keys = k.keys;
         it.table = k.table;
         it.j0 = j0;
-        it.n = min(k.kt, (min(Uk + k.ku, x1) - Uk - item_units(k.w)) >> (k.w - 1)) - j0;
+        it.n = min(k.kt, C::tiles(min(Uk + k.ku, x1) - Uk - C::item(k.w), k.w)) - j0;
         it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
         it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
         items[slot] = it;
         if constexpr (TREE) own[slot] = make_int2(k.q0, k.keys - k.tokens);
-        if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk + item_units(k.w), Uk + k.ku) : make_int4(0, 0, 0, 0);
+        if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk + C::item(k.w) + (TREE ? C::tile(k.w) - 1 : 0), Uk + k.ku) : make_int4(0, 0, 0, 0);
     };
-    // Items of a chunk that start before x1, but the last of them if x1 is among its first units.
+    // Items of a chunk that start before x1, but the last of them if x1 is among its first units (TREE: or in its first key tile).
     auto items_before = [&](const Chunk& k, int start, int x1) {
-        return k.items == 0 || start + item_units(k.w) >= x1 ? 0 : min(k.items, ceil_div(x1 - start - item_units(k.w), k.ku));
+        const int least = C::item(k.w) + (TREE ? C::tile(k.w) - 1 : 0);  // (the first key tile is before the cut)
+        return k.items == 0 || start + least >= x1 ? 0 : min(k.items, ceil_div(x1 - start - least, k.ku));
     };
     // Each thread takes a contiguous run of chunks: (0) the sums of their units and items; (1) with what comes before
     // known, the place where this CTA's share starts; (2) the first batch of its items.
@@ -393,9 +408,9 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 T = 0;
                 if (cta == 0 && tid == 0) raise_error(a.err, PKV_DEVERR_BAD_LENGTH);
             } else {
-                share = max(kMinShare, (ceil_div(T, ncta) + 1) & ~1);
+                share = max(C::kLeast, C::up(ceil_div(T, ncta)));
             }
-            if ((TREE ? shared_keys : !f.prefix) && M >= 2 * ncta && T / M >= kRoundUnits) rounds = min(kRounds, M / ncta - 1);
+            if ((TREE ? shared_keys : !f.prefix) && M >= 2 * ncta && T / M >= kRoundUnits * (TREE ? 5 : 1)) rounds = min(kRounds, M / ncta - 1);
             if (tid == 0) {
                 mine[5] = mine[12] = rounds;
                 mine[6] = 0;
@@ -448,6 +463,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     load += (first_unit[c + 1] - first_unit[c]) / (first_item[c + 1] - first_item[c]);
                 }
                 part_c = max(0, share - load);
+                if (TREE && part_c > 0) part_c = max(part_c, C::kLeast);
             }
             if (tid < rounds) {
                 const int item = tid * ncta + cta, c = chunk_of(item), m = item - first_item[c];

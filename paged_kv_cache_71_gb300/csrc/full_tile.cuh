@@ -21,7 +21,7 @@ struct FullArgs {
     int* share;          // stream units per CTA; 0: `points`
     int* points;         // [CTAs + 1] where the CTAs' parts of the stream start, when they differ
     int4* cuts;          // [CTAs] {first token, tokens | head << 16, U0, U1} of the item that the CTA's share starts inside
-                         // of, its key tiles at units [U0, U1) of the stream; U1 = 0: none
+                         // of: shares that start in (U0, U1) of the stream start with a later piece of it; U1 = 0: none
     int4* seq_plan;      // shared prefixes: [sequences] {first key tile's unit of KV head 0's item, units per item, row in the
                          // item, units of its key tiles}
     const int* prefix_blocks;  // [sequences] as the decode of the own blocks found them: > 0 if the row is to be joined
