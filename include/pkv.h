@@ -554,22 +554,23 @@ pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache,
  * frequencies below 2^24), and each result is rounded once, to the type of q_out
  * or of the cache (as pkv_reshape_and_cache rounds it).
  *   q, q_out: [num_tokens] rows of num_q_heads * head_dim elements, q_stride and
- *        q_out_stride elements apart.  q_out may be q with the same stride.  Both
- *        NULL with num_q_heads = 0: keys and values only.
+ *        q_out_stride elements apart.  q_out may be q with the same stride, and
+ *        overlaps no input otherwise.  Both NULL with num_q_heads = 0: keys and
+ *        values only.
  *   k_new, v_new: [num_tokens] rows of num_kv_heads * head_dim, k_stride and
  *        v_stride apart.  Both NULL: queries only; slot_mapping and the caches
  *        may then be NULL.  Queries, keys and values may be parts of one row (a
  *        fused projection's output).
  *   positions: int32 [num_tokens], any value.
- *   slot_mapping: as for pkv_reshape_and_cache.  Nothing is written for a token
- *        whose slot is negative (padding) or beyond the pool
- *        (PKV_DEVERR_BAD_SLOT): its q_out row stays too.
+ *   slot_mapping: as for pkv_reshape_and_cache (two tokens with the same slot
+ *        race).  Nothing is written for a token whose slot is negative (padding) or
+ *        beyond the pool (PKV_DEVERR_BAD_SLOT): its q_out row stays too.
  *   inv_freq: fp32 [rot_dim / 2] device array, scaled for long contexts as the
  *        model wants it; a value that is not finite gives NaN.
  * All tensors of src_dtype (f32 or bf16) and the caches 16-byte aligned, strides
  * multiples of 16 bytes.
  * Supported: rot_dim a multiple of 8 up to head_dim; the cache write's types,
- *   head_dim 64 and 128, any head counts.
+ *   head_dim 64 and 128, head counts up to num_q_heads + 2 * num_kv_heads = 2^20.
  */
 pkv_status pkv_rope_and_cache(void* q_out, const void* q, const void* k_new, const void* v_new, int32_t src_dtype,
                               int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -635,15 +636,15 @@ pkv_status pkv_paged_attention_tree_workspace_size(const pkv_cache_desc* cache, 
  * A run of no tokens gives 0, past_lens[s] and next token -1.  `accepted` entries that no
  * sequence owns are not written.
  *   k_caches, v_caches: HOST arrays of num_layers device pointers (read during the call),
- *        pools of the same geometry and dtype; `cache` describes one of them (its scales
- *        are not used).
+ *        pools of the same geometry and dtype that do not overlap; `cache` describes one of
+ *        them (its scales are not used).
  * The moved positions' blocks must be the sequence's own.  Output arrays must not overlap
  * one another or the inputs.
  * A malformed cu_q range, a run of more than PKV_MAX_COMMIT_RUN tokens, a negative length
  * or one past max_blocks_per_seq * S with the run sets PKV_DEVERR_BAD_LENGTH; such a
  * sequence is as one without a run (its `accepted` entries -1, where its range is one).
  * A table entry outside the pool sets PKV_DEVERR_BAD_BLOCK and leaves the token that it
- * concerns where it is.
+ * concerns where it is (the lengths and `accepted` are as without the error).
  * Supported: every cache type and shape, num_seqs <= 8192, num_layers <= PKV_MAX_LAYERS.
  */
 #define PKV_MAX_LAYERS 128

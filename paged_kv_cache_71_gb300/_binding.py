@@ -598,6 +598,8 @@ class LayerCaches:
         for t in k_caches + v_caches:
             if t.dtype is not first.dtype or t.shape != first.shape or t.device != first.device or not t.is_contiguous():
                 raise PkvError(1, "LayerCaches", "the layers' pools must be contiguous, of one shape, type and device")
+        if len({t.data_ptr() for t in k_caches + v_caches}) < 2 * len(k_caches):
+            raise PkvError(1, "LayerCaches", "two of the layers' pools are the same memory")
         self.tensors = k_caches, v_caches  # kept alive
         self.device = first.get_device()
         self.num_layers = len(k_caches)
@@ -615,10 +617,17 @@ def pkv_commit_tree(layers: LayerCaches, block_tables, cu_q, past_lens, parents,
         _dims(func, past_lens=(past_lens, 1), block_tables=(block_tables, 2), parents=(parents, 1))
     shape, runs, width = past_lens.shape, parents.shape, block_tables.shape[1]
     n, tokens = shape[0], runs[0]
-    if not (layers.device == dev and _word(device_error, dev) and _fits(past_lens, i32, shape, dev)
-            and _fits(block_tables, i32, (n, width), dev) and _fits(cu_q, i32, (n + 1,), dev) and _fits(parents, i32, runs, dev)
-            and _fits(draft_tokens, i32, runs, dev) and _fits(target_tokens, i32, runs, dev) and _fits(accepted, i32, runs, dev)
-            and _fits(num_accepted, i32, shape, dev) and _fits(seq_lens, i32, shape, dev) and _fits(next_tokens, i32, shape, dev)
+    if not (block_tables.dtype is cu_q.dtype is past_lens.dtype is parents.dtype is draft_tokens.dtype is target_tokens.dtype
+            is accepted.dtype is num_accepted.dtype is seq_lens.dtype is next_tokens.dtype is i32
+            and block_tables.shape[0] == n and cu_q.dim() == 1 and cu_q.shape[0] == n + 1
+            and draft_tokens.shape == runs == target_tokens.shape and accepted.shape == runs
+            and num_accepted.shape == shape == seq_lens.shape and next_tokens.shape == shape
+            and block_tables.is_contiguous() and cu_q.is_contiguous() and past_lens.is_contiguous() and parents.is_contiguous()
+            and draft_tokens.is_contiguous() and target_tokens.is_contiguous() and accepted.is_contiguous()
+            and num_accepted.is_contiguous() and seq_lens.is_contiguous() and next_tokens.is_contiguous()
+            and layers.device == block_tables.get_device() == cu_q.get_device() == past_lens.get_device() == parents.get_device()
+            == draft_tokens.get_device() == target_tokens.get_device() == accepted.get_device() == num_accepted.get_device()
+            == seq_lens.get_device() == next_tokens.get_device() == dev and _word(device_error, dev)
             and (keep_blocks is None or _fits(keep_blocks, i32, shape, dev))):
         _refuse(func, _device(), device_error, past_lens=(past_lens, _I32, (n,)), block_tables=(block_tables, _I32, (n, width)),
                 cu_q=(cu_q, _I32, (n + 1,)), parents=(parents, _I32, (tokens,)), draft_tokens=(draft_tokens, _I32, (tokens,)),

@@ -151,6 +151,7 @@ def _rope(q_out=PTR, q=PTR, k=PTR, v=PTR, src=B.PKV_BF16, strides=(1024, 1024, 2
     (dict(scale=float("inf")), 1), (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(slots=ODD), 1), (dict(strides=(1024, 1020, 256, 256)), 1),
     (dict(strides=(1024, 1016, 256, 256)), 1), (dict(strides=(0, 1024, 256, 256)), 1), (dict(strides=(1024, 1024, 248, 256)), 1),
     (dict(strides=(1024, 1024, 256, -256)), 1), (dict(desc=_desc(block_size=5)), 2),
+    (dict(heads=1 << 20, strides=(1 << 27, 1 << 27, 256, 256)), 3),
 ])
 def test_rope_checks(kw, status):
     assert _rope(**kw) == status, pkv.pkv_last_error()
@@ -224,15 +225,18 @@ def test_layer_caches_refuse():
                    ([_z(4, 16, 256, dtype=BF)], [k]), ([k.double()], [k.double()]), ([k[:, ::2]], [k[:, ::2]])):
         with pytest.raises(pkv.PkvError):
             pkv.LayerCaches(ks, vs)
-    layers = pkv.LayerCaches([k, k], [k, k])
-    assert layers.num_layers == 2 and layers.desc.num_blocks == 4 and layers.k_pointers[1] == k.data_ptr()
+    with pytest.raises(pkv.PkvError, match="same memory"):  # every layer's tokens would move twice
+        pkv.LayerCaches([k, k], [k.clone(), k.clone()])
+    pools = [k.clone() for _ in range(4)]
+    layers = pkv.LayerCaches(pools[:2], pools[2:])
+    assert layers.num_layers == 2 and layers.desc.num_blocks == 4 and layers.k_pointers[1] == pools[1].data_ptr()
 
 
 def _bcommit(**o):
     k = _z(4, 16, 2, 128, dtype=BF)
     a = dict(bt=_z(2, 4), cu=_z(3), past=_z(2), parents=_z(9), draft=_z(9), target=_z(9), accepted=_z(9), count=_z(2), lens=_z(2), nxt=_z(2), keep=_z(2))
     a.update(o)
-    pkv.pkv_commit_tree(pkv.LayerCaches([k], [k]), a["bt"], a["cu"], a["past"], a["parents"], a["draft"], a["target"], a["accepted"], a["count"],
+    pkv.pkv_commit_tree(pkv.LayerCaches([k], [k.clone()]), a["bt"], a["cu"], a["past"], a["parents"], a["draft"], a["target"], a["accepted"], a["count"],
                         a["lens"], a["nxt"], a["keep"])
 
 
