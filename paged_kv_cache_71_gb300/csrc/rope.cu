@@ -25,6 +25,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;      // most units of a thread
 constexpr int kMaxTokens = 4;  // most tokens of a CTA
+// CTAs that an SM's registers have to hold.  No bound, 3, 4, 5: 8192 bf16 prompt tokens (32 / 8 heads) 41.7 / 34.4 / 32.3 / 32.7
+// us, 1013 tokens of 64 / 8 heads into an FP8 cache 11.2 / 9.3 / 7.8 / 9.6 (floors 29.7 and 5.8; 2 us of each is the launch).
+constexpr int kCtas = 4;
 
 // f turns per radian times 2^64, mod 2^64, for a finite f: the mantissa times floor(2^64 / (2 pi)), shifted by the exponent.
 // (Frequencies of 2^24 and more, far beyond the one radian per position that models use, lose bits.)
@@ -81,7 +84,7 @@ __device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const f
         if constexpr (T == PKV_F32) {
             w[i] = __float_as_uint(f[i]);
         } else if constexpr (T == PKV_BF16) {
-            w[i] = float_to_bf16_bits(f[2 * i]) | static_cast<uint32_t>(float_to_bf16_bits(f[2 * i + 1])) << 16;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
         } else {  // the cache write's conversions: an IEEE division, then round to nearest even, saturated
             w[i] = 0;
 #pragma unroll
@@ -108,7 +111,7 @@ __device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const f
 
 // Grid: x runs of `per_cta` tokens, y parts of the heads (queries, keys and values in a row).  V: elements of a group.
 template <int SRC, int DST, int V>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, int per_cta) {
+__global__ void __launch_bounds__(kThreads, kCtas) rope_and_cache_kernel(const RopeArgs a, int per_cta) {
     // cos, sin of each token's pairs, two pairs to 16 bytes; those that the threads of a head read at a time side by side
     __shared__ float4 turn[kMaxTokens][32];
     __shared__ int64_t slot_of[kMaxTokens];  // -1: nothing of the token is written
