@@ -601,7 +601,8 @@ pkv_status pkv_rope_and_cache(void* q_out, const void* q, const void* k_new, con
  * A malformed cu_q range, a length outside [0, max_blocks_per_seq * S], one below n, or
  * a run longer than 64 * mask_words sets PKV_DEVERR_BAD_LENGTH and leaves that
  * sequence's rows unwritten; a table entry outside the pool sets PKV_DEVERR_BAD_BLOCK.
- * Supported: the types, shapes and limits of pkv_paged_cross_attention with cu_q.
+ * Supported: the types, shapes and limits of pkv_paged_cross_attention with cu_q, the
+ *   last of them with (10 * key tiles + 35) in place of (2 * key tiles + 32).
  */
 pkv_status pkv_paged_attention_tree(void* out, const void* q, int32_t q_dtype, int32_t total_q_tokens,
                                     const int32_t* cu_q, const int32_t* kv_lens, const uint64_t* tree_mask,

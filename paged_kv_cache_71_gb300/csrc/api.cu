@@ -1587,6 +1587,7 @@ PKV_API pkv_status pkv_rope_and_cache(void* q_out, const void* q, const void* k_
         return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes and hold a token's heads");
     if (!aligned4(positions) || !aligned4(inv_freq) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return fail(PKV_ERR_INVALID_ARG, "positions and inv_freq must be 4-byte aligned, slot_mapping 8-byte");
+    if (num_tokens > INT32_MAX - 4096) return fail(PKV_ERR_OUT_OF_RANGE, "num_tokens %d", num_tokens);
     if (num_q_heads + 2ll * Hkv > 1 << 20) return fail(PKV_ERR_OUT_OF_RANGE, "more than 2^20 heads in a token's rows");
     DeviceInfo di;
     if ((st = device_info(&di)) != PKV_OK) return st;

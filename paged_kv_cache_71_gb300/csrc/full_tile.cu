@@ -1002,11 +1002,11 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                                 const uint4 was = *at;
                                 const uint4 is = make_uint4(finite_or_zero<NARROW>(was.x), finite_or_zero<NARROW>(was.y),
                                                             finite_or_zero<NARROW>(was.z), finite_or_zero<NARROW>(was.w));
-                                if (is.x != was.x || is.y != was.y || is.z != was.z || is.w != was.w) {
-                                    mine[13] = 1;
-                                    __threadfence_block();
-                                    *at = is;
-                                }
+                                const bool odd = is.x != was.x || is.y != was.y || is.z != was.z || is.w != was.w;
+                                if (odd) mine[13] = 1;
+                                // (of two query tiles' groups each writes, whether or not the other has: what its own products
+                                // read is then ordered by its own fence)
+                                if (odd || pair) *at = is;
                             } else {
                                 *at = make_uint4(0u, 0u, 0u, 0u);
                             }

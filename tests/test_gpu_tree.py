@@ -309,6 +309,62 @@ def test_repeated_calls_streams_and_graphs():
     b.verify("replayed with other queries")
 
 
+def test_two_calls_at_once():
+    """Other batches, caches and sizes on two streams, each with its own workspace; masks as uint64."""
+    a = Batch(trees(11, [16, 40, 8, 1]), [600, 30, 2000, 64], 2, 4, 16, "bf16", seed=11).device()
+    b = Batch(trees(12, [3] * 40), [900] * 40, 1, 8, 8, "int8", seed=12).device()
+    a.dm = a.dm.view(torch.uint64)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a.run(stream=s)
+        b.run(stream=t)
+    a.verify("first stream")
+    b.verify("second stream")
+    assert int(a.err) == 0 and int(b.err) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_queries_and_values_that_are_no_numbers_in_pairs_of_tiles(kv):
+    """Runs of more than 128 rows: both groups of a tile pair meet the same values; a NaN query stays in its row."""
+    n = 60
+    b = Batch([[1 << i for i in range(n)], [1 << i for i in range(n)]], [64, 500], 1, 4, 16, kv, seed=13)
+    for s in range(2):
+        blk, off = b.place(s, b.lens[s] - n + 17)
+        if kv == "fp8":
+            b.v.view(torch.uint8)[blk, off] = 0x7f
+        else:
+            b.v[blk, off] = float("inf")
+    if kv == "bf16":
+        b.q[3] = float("nan")
+    b.device().run()
+    torch.cuda.synchronize()
+    for s in range(2):
+        a, L = b.cu[s], b.lens[s]
+        rest = [i for i in range(n) if i != 17 and a + i != 3]
+        k, v = gather(b.k, b.tables[s], L), gather(b.v, b.tables[s], L)
+        q = b.q[a:a + n].nan_to_num(0.0)
+        ref, bound = attend_masked(q, k, v, seen_keys(n, L, b.runs[s]), b.scale, kv, b.ks, b.vs)
+        check(b.out[a:a + n][rest], ref[rest], bound[rest], f"{kv}, sequence {s}")
+        got = b.out[a + 17].float()
+        assert torch.isnan(got).all() if kv == "fp8" else (got == float("inf")).all()
+    if kv == "bf16":
+        assert torch.isnan(b.out[3].float()).all()
+
+
+def test_far_tables_and_pools():
+    """Blocks whose elements lie past 2^31."""
+    b = Batch(trees(14, [8, 5]), [300, 40], 8, 4, 32, "bf16", seed=14).device()
+    nb = (1 << 31) // (32 * 8 * 128) + 200
+    big_k = torch.zeros(nb, 32, 8, 128, dtype=torch.bfloat16, device="cuda")
+    big_v = torch.zeros_like(big_k)
+    shift = nb - b.dk.shape[0]
+    big_k[shift:], big_v[shift:] = b.dk, b.dv
+    b.dk, b.dv, b.dt = big_k, big_v, torch.where(b.dt >= 0, b.dt + shift, b.dt)
+    b.desc = pkv.CacheDesc.for_cache(b.dk)
+    b.run().verify("far")
+
+
 def test_many_sequences():
     """2048 runs of none to three tokens."""
     r = random.Random(3)
