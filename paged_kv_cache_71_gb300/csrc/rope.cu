@@ -75,8 +75,23 @@ struct Group {
     }
 };
 
+// f / scale, as the cache write divides (IEEE).  Of a power of two the product with its inverse, which is the same number:
+// 8192 tokens of 16 / 8 heads of 64 into an FP8 cache 16.3 us by division, 13.0 by product (12.3 with two codes a conversion).
+template <int V>
+__device__ __forceinline__ void divide(float (&f)[V], float scale) {
+    const uint32_t u = __float_as_uint(scale), e = u >> 23;
+    if ((u & 0x7fffffu) == 0 && e >= 1 && e <= 253) {
+        const float inv = __uint_as_float((254 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] /= scale;
+    }
+}
+
 template <int T, int V>
-__device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const float (&f)[V], float scale) {
+__device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const float (&f)[V]) {
     constexpr int kBytes = T == PKV_F32 ? 4 : T == PKV_BF16 ? 2 : 1, kWords = V * kBytes / 4;
     uint32_t w[kWords];
 #pragma unroll
@@ -85,13 +100,15 @@ __device__ __forceinline__ void store_group(uint8_t* base, int64_t elem, const f
             w[i] = __float_as_uint(f[i]);
         } else if constexpr (T == PKV_BF16) {
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-        } else {  // the cache write's conversions: an IEEE division, then round to nearest even, saturated
+        } else if constexpr (T == PKV_FP8_E4M3) {  // the cache write's conversions: round to nearest even, saturated
+            uint16_t lo, hi;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[4 * i + 1]), "f"(f[4 * i]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[4 * i + 3]), "f"(f[4 * i + 2]));
+            w[i] = lo | static_cast<uint32_t>(hi) << 16;
+        } else {
             w[i] = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float y = f[4 * i + k] / scale;
-                w[i] |= static_cast<uint32_t>(T == PKV_INT8 ? float_to_s8_sym(y) : float_to_e4m3_sat(y)) << (8 * k);
-            }
+            for (int k = 0; k < 4; ++k) w[i] |= static_cast<uint32_t>(float_to_s8_sym(f[4 * i + k])) << (8 * k);
         }
     }
     uint8_t* p = base + elem * kBytes;
@@ -194,16 +211,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_and_cache_kernel(const R
         }
         if (is_q) {
             const int64_t at = (t0 + t) * a.q_out_stride + (static_cast<int64_t>(h) << a.d_shift);
-            store_group<SRC, V>(a.q_out, at + first, p, 1.f);
-            store_group<SRC, V>(a.q_out, at + second, q, 1.f);
+            store_group<SRC, V>(a.q_out, at + first, p);
+            store_group<SRC, V>(a.q_out, at + second, q);
         } else {
             const int kv = h - (is_k ? a.Hq : a.Hq + a.Hkv);
             uint8_t* dst = is_k ? a.k_cache : a.v_cache;
-            const float* hs = is_k ? a.k_head : a.v_head;
-            const float scale = hs ? __ldg(hs + kv) : is_k ? a.k_scale : a.v_scale;
+            if constexpr (DST == PKV_FP8_E4M3 || DST == PKV_INT8) {
+                const float* hs = is_k ? a.k_head : a.v_head;
+                const float scale = hs ? __ldg(hs + kv) : is_k ? a.k_scale : a.v_scale;
+                divide(p, scale);
+                divide(q, scale);
+            }
             const int64_t at = (slot * a.Hkv + kv) << a.d_shift;
-            store_group<DST, V>(dst, at + first, p, scale);
-            store_group<DST, V>(dst, at + second, q, scale);
+            store_group<DST, V>(dst, at + first, p);
+            store_group<DST, V>(dst, at + second, q);
         }
     }
 }

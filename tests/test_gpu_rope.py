@@ -210,6 +210,25 @@ def test_scales_per_head_and_saturation(dst):
     c.run().verify(f"{dst} head scales")
 
 
+@pytest.mark.parametrize("dst", ["fp8", "int8"])
+@pytest.mark.parametrize("src", ["f32", "bf16"])
+def test_codes_under_scales_of_all_sizes(src, dst):
+    """At position 0 keys are not turned: codes as the plain cache write makes them, whatever the scale (powers of two are
+    multiplied by their inverse, others divide).  Keys are compared as numbers: of a pair (-0, y) with y < 0 the turned first
+    element is -0 * 1 - y * 0 = -0 - (-0) = +0."""
+    c = Call(33, 4, 2, 128, 128, src, dst, seed=11)
+    c.dp.zero_()
+    for scale in (2.0 ** -149, 2.0 ** -127, 2.0 ** -126, 2.0 ** -30, 0.3, 0.5, 1.0, 3.0, 2.0 ** 40, 2.0 ** 126, 2.0 ** 127, 1e38):
+        desc = pkv.CacheDesc.for_cache(c.kc, scale, scale)
+        kc, vc = torch.zeros_like(c.kc), torch.zeros_like(c.vc)
+        kd, vd = torch.zeros_like(c.kc), torch.zeros_like(c.vc)
+        x = torch.cat([c.dk[:16], c.dk[16:] * scale * 7]).to(c.dk.dtype)
+        pkv.pkv_reshape_and_cache(x, c.dv, c.ds, kc, vc, desc)
+        pkv.pkv_rope_and_cache(None, None, x, c.dv, c.dp, c.ds, c.di, kd, vd, desc)
+        assert torch.equal(vc.view(torch.uint8), vd.view(torch.uint8)), scale
+        assert torch.equal(kc.float(), kd.float()), scale
+
+
 def test_slots_beyond_the_pool():
     c = Call(6, 4, 2, 128, 128, "bf16", "bf16", seed=8)
     c.slots[2] = c.kc.shape[0] * 16
