@@ -563,6 +563,8 @@ def pkv_paged_attention_tree(out, q, cu_q, kv_lens, tree_mask, k_cache, v_cache,
     tokens, heads, D = q.shape
     caches, width = (cache.num_blocks, cache.block_size, cache.num_kv_heads, D), block_tables.shape[-1]
     words = 0 if tree_mask is None else tree_mask.shape[1]
+    if tree_mask is not None and words == 0:
+        raise PkvError(1, func, "tree_mask has no words (a chain has no mask: None)")
     if not (D == cache.head_dim and q.dtype in _FLOATS and _DTYPE_CODE.get(k_cache.dtype) == cache.dtype and _room(workspace, dev)
             and _word(device_error, dev)
             and _fits(q, out.dtype, out.shape, dev) and out.is_contiguous() and out.get_device() == dev
@@ -577,7 +579,7 @@ def pkv_paged_attention_tree(out, q, cu_q, kv_lens, tree_mask, k_cache, v_cache,
                 cu_q=(cu_q, _I32, (n + 1,)), tree_mask=(tree_mask, _MASK, (tokens, words)))
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     status = L.pkv_paged_attention_tree(out.data_ptr(), q.data_ptr(), _DTYPE_CODE[q.dtype], tokens, cu_q.data_ptr(),
-                                        kv_lens.data_ptr(), _ptr(tree_mask), words, k_cache.data_ptr(), v_cache.data_ptr(),
+                                        kv_lens.data_ptr(), _ptr(tree_mask), words if tokens else 0, k_cache.data_ptr(), v_cache.data_ptr(),
                                         ctypes.byref(cache), block_tables.data_ptr(), width, n, heads, float(scale), ws, ws_bytes,
                                         _ptr(device_error), _stream(stream, dev))
     if status:

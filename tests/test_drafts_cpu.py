@@ -187,7 +187,7 @@ def _btree(**o):
 
 @pytest.mark.parametrize("kw,text", [
     (dict(q=_z(16, 128, dtype=BF)), "q has shape"), (dict(bt=_z(8)), "block_tables has shape"), (dict(mask=_z(2, dtype=torch.int64)), "tree_mask has shape"),
-    (dict(mask=_z(3, 1, dtype=torch.int64)), "tree_mask has shape"), (dict(mask=_z(2, 1)), "tree_mask has dtype"),
+    (dict(mask=_z(3, 1, dtype=torch.int64)), "tree_mask has shape"), (dict(mask=_z(2, 0, dtype=torch.int64)), "no words"), (dict(mask=_z(2, 1)), "tree_mask has dtype"),
     (dict(mask=_z(2, 4, dtype=torch.int64)[:, ::2]), "tree_mask must be contiguous"), (dict(cu=_z(2)), "cu_q has shape"),
     (dict(lens=_z(2, dtype=torch.int64)), "kv_lens has dtype"), (dict(k=_z(4, 16, 2, 128, dtype=FP8)), "k_cache has dtype"),
     (dict(desc=_desc(B.PKV_INT8)), "k_cache has dtype"), (dict(out=_z(2, 8, 128)), "out has dtype"), (dict(), "CUDA"),

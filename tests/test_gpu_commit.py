@@ -200,6 +200,12 @@ def test_bad_blocks():
         b.err.zero_()
 
 
+def test_no_tokens_at_all():
+    b = Batch([[], [], []], [0, 16, 37], 10).device()
+    b.run().verify("no runs")
+    assert int(b.err) == 0
+
+
 def test_without_blocks_to_keep_on_a_stream_and_from_a_graph():
     b = Batch(trees(9, [12, 30]), [5, 17], 9).device()
     s = torch.cuda.Stream()

@@ -309,6 +309,16 @@ def test_repeated_calls_streams_and_graphs():
     b.verify("replayed with other queries")
 
 
+@pytest.mark.parametrize("masked", [True, False])
+def test_no_tokens_at_all(masked):
+    """A step in which no sequence drafts: nothing is written, nothing refused."""
+    b = Batch([[], []] if masked else [0, 0], [40, 3], 2, 4, 16, "bf16", seed=15).device()
+    assert b.dq.shape[0] == 0 and (b.dm is not None) == masked
+    b.run()
+    torch.cuda.synchronize()
+    assert int(b.err) == 0
+
+
 def test_two_calls_at_once():
     """Other batches, caches and sizes on two streams, each with its own workspace; masks as uint64."""
     a = Batch(trees(11, [16, 40, 8, 1]), [600, 30, 2000, 64], 2, 4, 16, "bf16", seed=11).device()
