@@ -814,6 +814,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                                                (lane & 1 ? g / kStages - 1 : g / kSlots) & 1, a.timeout_ns);
                         ok = __all_sync(kFull, ok);
                         if (!ok) break;
+                        __syncwarp();  // a vote orders no memory: what either half of the lanes has seen, all have after this
                         const uint8_t* src = smem + PL::kOffStg + (is_v * PL::kSlots + slot) * kStgSlot + r * 128;
                         uint8_t* dst = smem + (is_v ? PL::kOffV : PL::kOffK) + st * kStage + r * 128;
                         // four pieces of 16 codes at a time, their loads before the stores (which the compiler may not pass)
