@@ -110,7 +110,8 @@ constexpr int kFKFull = 0, kFKEmpty = 8, kFVFull = 16, kFVEmpty = 24;  // + stag
 constexpr int kFS = 32, kFP = 36, kFPV = 40;        // + 2 * group + buffer: scores written, P written, P V done
 constexpr int kFQ = 44, kFO = 48;                   // + group: Q landed, O complete
 constexpr int kFMl = 50, kFTaken = 52;              // + owner: the other group's (m, l) are in shared memory; owner has its O
-constexpr int kFZero = 54;                          // V rows past the last key zeroed (items of two query tiles)
+constexpr int kFZero = 54;                          // V rows past the last key zeroed (items of two query tiles); TREE: an
+                                                    // item's masked tiles looked at, by both groups
 constexpr int kFVThere = 55;                        // + group: V with rows past the last key has landed
 constexpr int kFDrain = 57;
 constexpr int kFStg = 58, kFStgFree = 66;           // + 4 * (V ? 1 : 0) + slot
@@ -124,9 +125,10 @@ constexpr int kFMlOut = kFItems + 32 * kBatch;      // (m, l) of the other group
 constexpr int kFUnits = kFMlOut + 2 * 128 * 8;      // the chunks' first units, [kMaxSeqs + 1]
 constexpr int kFFirst = kFUnits + 4 * (kMaxSeqs + 1);  // and first items
 constexpr int kFEnd = kFFirst + 4 * (kMaxSeqs + 1);
-static_assert(kFMine + 56 <= kFItems, "meta slots overlap");
+static_assert(kFMine + 52 <= kFItems, "meta slots overlap");
 constexpr int kFOwn = kFEnd;                        // TREE: the listed items' runs, int2 {first token, keys before its own}
-constexpr int kFTreeEnd = kFOwn + 8 * kBatch;
+constexpr int kFOdd = kFOwn + 8 * kBatch;           // and whether a value of theirs is no finite number, ints
+constexpr int kFTreeEnd = kFOdd + 4 * kBatch;
 static_assert(kFOwn % 8 == 0, "int2 alignment");
 
 // One CTA's part of an item
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     Item* items = reinterpret_cast<Item*>(meta + kFItems);
     float2* ml_out = reinterpret_cast<float2*>(meta + kFMlOut);
     int2* own = reinterpret_cast<int2*>(meta + kFOwn);  // TREE only
+    volatile int* odd_values = reinterpret_cast<volatile int*>(meta + kFOdd);
     int* empty = reinterpret_cast<int*>(ml_out);  // while the plan is made: chunks without keys
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, ncta = gridDim.x;
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         if (i >= kFP && i < kFP + 4) count = 128;
         if (i >= kFMl && i <= kFZero) count = 128;
         if ((i >= kFKEmpty && i < kFVFull) || (i >= kFVEmpty && i < kFS)) count = 2;
+        if (TREE && i == kFZero) count = 256;
         if (i == kFDrain) count = 4;
         if (NARROW == 2 && (i < kFKEmpty || (i >= kFVFull && i < kFVEmpty) || i >= kFStgFree)) count = 2;
         mbar_init(bar + 8 * i, count);
@@ -277,7 +281,6 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         mine[11] = 0;
-        if constexpr (TREE) mine[13] = 0;
         prefetch_tensormap(&qmap);
     }
     if (warp == 8 && lane == 0) prefetch_tensormap(&kmap);
@@ -321,7 +324,10 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         it.head_pair = h | ((it.tokens > rows_q ? 1 : 0) << 16);
         it.rec = !(f.prefix || it.n < k.kt) ? 0 : j0 > 0 ? 2 : 1;
         items[slot] = it;
-        if constexpr (TREE) own[slot] = make_int2(k.q0, k.keys - k.tokens);
+        if constexpr (TREE) {
+            own[slot] = make_int2(k.q0, k.keys - k.tokens);
+            odd_values[slot] = 0;
+        }
         if (first) f.cuts[cta] = j0 > 0 ? make_int4(it.q_row, it.tokens | (h << 16), Uk + C::item(k.w) + (TREE ? C::tile(k.w) - 1 : 0), Uk + k.ku) : make_int4(0, 0, 0, 0);
     };
     // Items of a chunk that start before x1, but the last of them if x1 is among its first units (TREE: or in its first key tile).
@@ -860,6 +866,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
         int o_mine = 0, o_other = 0;          // items of this group, of the other one
         int joins_mine = 0, joins_other = 0;  // items that this group joined, that the other one did
         int zeroed = 0;                       // key tiles whose V rows past the last key it zeroed
+        int pairs = 0;                        // TREE: items of two query tiles
         bool lent = false;                    // the other group still has to read this group's O
         auto next_item = [&](int i, int n) {  // this group's first item from the i-th on
             while (i < n && first_tile(t, i, items[i].head_pair >> 16) >= items[i].n) ++i;
@@ -1004,7 +1011,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                                 const uint4 is = make_uint4(finite_or_zero<NARROW>(was.x), finite_or_zero<NARROW>(was.y),
                                                             finite_or_zero<NARROW>(was.z), finite_or_zero<NARROW>(was.w));
                                 const bool odd = is.x != was.x || is.y != was.y || is.z != was.z || is.w != was.w;
-                                if (odd) mine[13] = 1;
+                                if (odd) odd_values[i] = 1;
                                 // (of two query tiles' groups each writes, whether or not the other has: what its own products
                                 // read is then ordered by its own fence)
                                 if (odd || pair) *at = is;
@@ -1026,6 +1033,8 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     tc_fence_before();
                     mbar_arrive(bar + 8 * (kFP + 2 * t + b));
                 }
+                // TREE: what the other group zeroed first, this one did not meet: they tell each other of it (below)
+                if (TREE && NARROW != 2 && pair && ok) mbar_arrive(bar + 8 * kFZero);
                 ++o_mine;
                 if (pair || split) ++o_other;
                 if (split && t == owner) ++joins_mine;
@@ -1043,6 +1052,10 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                 if (!warp_wait(bar + 8 * (kFO + t), (o_mine - 1) & 1, a.timeout_ns) ||
                     (split && (!warp_wait(bar + 8 * (kFMl + t), (joins_mine - 1) & 1, a.timeout_ns) ||
                                !warp_wait(bar + 8 * (kFO + (t ^ 1)), (o_other - 1) & 1, a.timeout_ns)))) {
+                    give_up();
+                    break;
+                }
+                if (TREE && NARROW != 2 && pair && !warp_wait(bar + 8 * kFZero, pairs++ & 1, a.timeout_ns)) {
                     give_up();
                     break;
                 }
@@ -1090,7 +1103,7 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                         __syncwarp();  // TMEM is read by whole warps: the rows that are none wait for the others
                     }
                     if (rec && valid) f.rec_ml[rec_row] = make_float2(m_ref, l_run);
-                    if (TREE && NARROW != 2 && valid && mine[13])
+                    if (TREE && NARROW != 2 && valid && odd_values[i])
                         add_odd<NARROW>(a, f, it, own[i], it.q_row + (row >> g_shift), h, rec ? rec_o : nullptr,
                                         reinterpret_cast<__nv_bfloat16*>(out_o));
                 }
