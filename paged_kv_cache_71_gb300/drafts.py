@@ -43,7 +43,7 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
     * "llama3": by wavelength against original_length L: f_i above L / high_freq_factor's frequency, f_i / s below
       L / low_freq_factor's, in between (1 - w) f_i / s + w f_i with w linear in L f_i / (2 pi)
     * "yarn":   f_i for pairs that turn beta_fast times or more within L, f_i / s for those below beta_slow turns, a ramp
-      linear in i between the two pairs' indexes; rope_scale = 0.1 ln(s) + 1 for s > 1
+      linear in i between the two pairs' indexes (rounded down, 0 at least, and up); rope_scale = 0.1 ln(s) + 1 for s > 1
     """
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim {rot_dim} is not a positive even number")
@@ -72,7 +72,9 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
         def pair_of(turns):  # the pair (a real number) that turns that often within original_length
             return half * math.log(original_length / (turns * 2 * math.pi)) / math.log(base)
 
-        lo, hi = max(0, math.floor(pair_of(beta_fast))), min(half - 1, math.ceil(pair_of(beta_slow)))
+        # (hi may lie behind the last pair, where that one still turns more than beta_slow times, or before the first one)
+        hi = math.ceil(pair_of(beta_slow))
+        lo = min(max(0, math.floor(pair_of(beta_fast))), hi)
         w = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
         f = (1 - w) * f + w * f / factor
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
