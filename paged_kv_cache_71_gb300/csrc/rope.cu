@@ -6,9 +6,9 @@
 // in fp32, rounded once to the type of the output or the cache.
 //
 // Angles: p f loses its fraction of a turn in fp32 long before p reaches a long context's end, so the angle is kept in turns
-// as a 64-bit fraction: phase = f / (2 pi) * 2^64, once per CTA and frequency by an integer product with 2^64 / (2 pi), and
-// p * phase mod 2^64 is the reduced angle, off by at most |p| 2^-63 turns.  Its upper 32 bits (2^-32 turns) go to
-// sincospi.  Every (token, pair) is computed once for all heads of a CTA, through shared memory.
+// as a 64-bit fraction: phase = f / (2 pi) * 2^64, by an integer product with 2^96 / (2 pi), and p * phase mod 2^64 is the
+// reduced angle, off by less than 1.51 |p| 2^-64 turns for f below 2^24.  Its upper 32 bits (2^-32 turns) go to sincospi.
+// Every (token, pair) is computed once for all heads of a CTA, through shared memory.
 //
 // Bound by HBM (large calls) or launch latency.  A thread's unit is two 16-byte groups of one head's elements, of the first and
 // the second half of the pairs or one behind the other (two 8-byte groups of bf16 where the rotated part is no multiple of
@@ -29,15 +29,20 @@ constexpr int kMaxTokens = 4;  // most tokens of a CTA
 // us, 1013 tokens of 64 / 8 heads into an FP8 cache 11.2 / 9.3 / 7.8 / 9.6 (floors 29.7 and 5.8; 2 us of each is the launch).
 constexpr int kCtas = 4;
 
-// f turns per radian times 2^64, mod 2^64, for a finite f: the mantissa times floor(2^64 / (2 pi)), shifted by the exponent.
-// (Frequencies of 2^24 and more, far beyond the one radian per position that models use, lose bits.)
+// f turns per radian times 2^64, mod 2^64, for a finite f below 2^24: the mantissa times the first 96 bits of 1 / (2 pi), shifted
+// by the exponent (a reduction after Payne and Hanek).  Off by less than 1.51: one for the bits shifted out, half of 1.004
+// for those of the product that are not computed.  With the constant's first 64 bits alone the error was half of f more, so
+// that at position 2^31 - 1 f = 1000 was off by 4e-7 radians, 2^23 by 3e-3; 8192 tokens of 8 / 1 heads took 9.8 us, with 96
+// bits 10.0.  (Larger f, far beyond the one radian per position that models use, lose bits.)
 __device__ __forceinline__ uint64_t turns(float f) {
-    constexpr uint64_t kPerRadian = 0x28be60db9391054aull;  // floor(2^64 / (2 pi))
+    constexpr uint64_t kPerRadian = 0x28be60db9391054aull;  // floor(2^96 / (2 pi)), its upper 64 bits
+    constexpr uint32_t kPerRadianLow = 0x7f09d5f4u;
     const uint32_t u = __float_as_uint(f);
     const int e = (u >> 23) & 255;
-    const uint64_t m = e ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu);
+    const uint32_t m = e ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu);
     const int right = 150 - max(e, 1);  // f = m * 2^-right
-    const uint64_t lo = m * kPerRadian, hi = __umul64hi(m, kPerRadian);
+    const uint64_t top = m * kPerRadian, lo = top + __umulhi(m, kPerRadianLow);
+    const uint64_t hi = __umul64hi(m, kPerRadian) + (lo < top);
     uint64_t t;
     if (right <= 0) t = right > -64 ? lo << -right : 0;
     else if (right < 64) t = (lo >> right) | (hi << (64 - right));
@@ -76,7 +81,7 @@ struct Group {
 };
 
 // f / scale, as the cache write divides (IEEE).  Of a power of two the product with its inverse, which is the same number:
-// 8192 tokens of 16 / 8 heads of 64 into an FP8 cache 16.3 us by division, 13.0 by product (12.3 with two codes a conversion).
+// 8192 tokens of 16 / 8 heads of 64 into an FP8 cache 16.3 us by division, 13.0 by product (12.5 with two codes a conversion).
 template <int V>
 __device__ __forceinline__ void divide(float (&f)[V], float scale) {
     const uint32_t u = __float_as_uint(scale), e = u >> 23;
