@@ -10,8 +10,10 @@
 // 16-byte column of the token rows, takes up to kBatch of them with loads before the stores, and what an earlier batch
 // overwrote lies at run indexes below its last j, which no later token comes from (i >= j).
 //
-// Bound by launch latency, then by HBM: every moved row is read and written once.  256 ragged trees of 32 layers (bf16, 8 heads
-// of 128; 78 MB): 15.0 us from a graph where 2 are the launch and 11.5 the bytes' at the measured copy rate; 8 trees 3.2 us.
+// Bound by latency: the launch, the run's loads, the walk, the table's, then a thread's loads and stores, few of them at a time
+// where little moves.  256 ragged trees of 32 layers (bf16, 8 heads of 128; 78 MB, 11.5 us at the measured copy rate) from graphs:
+// 19.3 us with pools that are not in L2 (six batches in turn), 14.7 with one batch over and over, most of which stays there.
+// 8 trees 3.6 / 3.3 us.
 #include <algorithm>
 
 #include "commit.cuh"
@@ -22,10 +24,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 8;
+// CTAs that an SM holds at a time (48 registers, 25 KB of shared memory).  The work split for 2, 3, 4, 5, 6, 8, 10, 16 of them: the 256
+// trees, not in L2, 31.5 / 24.0 / 21.3 / 19.2 / 19.2 / 20.7 / 20.1 / 20.4 us, 48 trees of 64 in 80 layers (FP8, 20 MB)
+// 11.0 / 9.5 / 8.9 / 8.4 / 8.5 / 8.3 / 9.8 / 9.8.
+constexpr int kCtas = 5;
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads) commit_tree_kernel(const __grid_constant__ CommitArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) commit_tree_kernel(const __grid_constant__ CommitArgs a) {
     __shared__ int parent[kMaxCommitRun], draft[kMaxCommitRun], target[kMaxCommitRun];
     __shared__ int path[kMaxCommitRun], from[kMaxCommitRun], to[kMaxCommitRun];
     __shared__ int counts[2];  // tokens of the path, moves
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) commit_tree_kernel(const __grid_cons
 
 cudaError_t launch_commit_tree(CommitArgs& a, int num_seqs, int sms, cudaStream_t stream) {
     // as many CTAs as the SMs hold at a time, a layer each at least
-    const int64_t fill = static_cast<int64_t>(sms) * (2048 / kThreads);
+    const int64_t fill = static_cast<int64_t>(sms) * kCtas;
     a.per_cta = static_cast<int>(std::max<int64_t>(1, (static_cast<int64_t>(num_seqs) * a.layers + fill - 1) / fill));
     a.per_cta = std::min(a.per_cta, a.layers);
     const dim3 grid(num_seqs, (a.layers + a.per_cta - 1) / a.per_cta);
