@@ -567,6 +567,7 @@ pkv_status pkv_paged_cross_attention_workspace_size(const pkv_cache_desc* cache,
  *        beyond the pool (PKV_DEVERR_BAD_SLOT): its q_out row stays too.
  *   inv_freq: fp32 [rot_dim / 2] device array, scaled for long contexts as the
  *        model wants it; a value that is not finite gives NaN.
+ *   rope_scale: finite and positive; 1 for none.
  * All tensors of src_dtype (f32 or bf16) and the caches 16-byte aligned, strides
  * multiples of 16 bytes.
  * Supported: rot_dim a multiple of 8 up to head_dim; the cache write's types,
