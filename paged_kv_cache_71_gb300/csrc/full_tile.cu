@@ -1055,7 +1055,11 @@ __global__ void __launch_bounds__(FullPlan<NARROW>::kThreads, 1)
                     give_up();
                     break;
                 }
-                if (TREE && NARROW != 2 && pair && !warp_wait(bar + 8 * kFZero, pairs++ & 1, a.timeout_ns)) {
+                // TREE: what the item's masked tiles held is known to all of them: of two query tiles' groups past kFZero, of one
+                // query tile's once every thread of this group has given its last P (and of the other its (m, l), above)
+                if (TREE && NARROW != 2 &&
+                    !(pair ? warp_wait(bar + 8 * kFZero, pairs++ & 1, a.timeout_ns)
+                           : warp_wait(bar + 8 * (kFP + 2 * t + ((c - 1) & 1)), ((c - 1) >> 1) & 1, a.timeout_ns))) {
                     give_up();
                     break;
                 }
